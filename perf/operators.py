@@ -280,7 +280,7 @@ def _run_own(s):
                                        s["blocks"], s["O"], ws=s["ws"])
     elif kind == "fork":
         F.focus_pages_release(s["pages"], s["dst"], s["none"])
-        F.focus_pages_fork(s["pages"], s["src"], s["dst"], s["keep"], s["status"])
+        F.focus_pages_fork(s["pages"], s["src"], s["dst"], s["keep"])
         F.focus_pages_own(s["pages"], s["dst"], s["first"], s["keep"], s["pairs"], s["n_pairs"], s["status"])
         F.focus_pages_copy(cache, s["pairs"], s["n_pairs"])
     else:
