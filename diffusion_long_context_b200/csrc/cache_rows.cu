@@ -1,0 +1,472 @@
+// Rows of the 8-bit paged cache: storing whole prompts, replacing single rows, reading back,
+// copying pages.
+//
+// All four only move bytes: a store reads 2 bytes and writes 1 per element, a load the other
+// way round, a copy 1 and 1. The scale of a page needs the largest magnitude of its rows
+// before the first code can be written, so a group of threads holds a whole page of one head
+// in registers between the two: page * d / 32 threads with four 16-byte vectors each.
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace focus {
+
+int check_cache(const focus_cache* c, const int32_t* table, int table_cols, bool n_mat_one) {
+  FOCUS_CHECK_ARG(c && c->k && c->v && c->k_scale && c->v_scale, "null pointer argument (cache)");
+  FOCUS_CHECK_ARG(c->format == FOCUS_CACHE_E4M3 || c->format == FOCUS_CACHE_INT8, "unknown cache format %d", c->format);
+  FOCUS_CHECK_ARG(c->n_mat >= 0 && c->n_pages >= 1 && c->Hkv >= 1, "bad cache sizes (n_mat=%d n_pages=%d Hkv=%d)",
+                  c->n_mat, c->n_pages, c->Hkv);
+  FOCUS_CHECK_ARG(!n_mat_one || c->n_mat == 1, "attention reads the cache of one layer (n_mat=%d)", c->n_mat);
+  if (c->d != 64 && c->d != 128) {
+    set_error("cache: d must be 64 or 128 (got %d)", c->d);
+    return FOCUS_ERR_UNSUPPORTED;
+  }
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) {
+    set_error("cache: page must be 16, 32, 64 or 128 (got %d)", c->page);
+    return FOCUS_ERR_UNSUPPORTED;
+  }
+  FOCUS_CHECK_ARG(static_cast<long long>(c->n_pages) * c->Hkv < (1LL << 31), "cache: n_pages * Hkv must be below 2^31");
+  FOCUS_CHECK_ARG(aligned16(c->k) && aligned16(c->v), "cache codes must be 16-byte aligned");
+  FOCUS_CHECK_ARG((reinterpret_cast<uintptr_t>(c->k_scale) & 3u) == 0 && (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) == 0,
+                  "cache scales must be 4-byte aligned");
+  FOCUS_CHECK_ARG(table && table_cols >= 1, "null table or no columns");
+  return FOCUS_OK;
+}
+
+namespace {
+
+struct RowArgs {
+  const uint4* X[2];           // K, V (bf16 rows)
+  uint2* code[2];              // codes, eight to a vector
+  float* scale[2];
+  uint4* out[2];               // load: bf16 rows
+  const int32_t* lens;
+  const int32_t* table;
+  const int32_t* rows;         // scatter
+  const int32_t* n_rows;
+  int table_cols, B, H, L, d, page, n_pages, cap, start;
+  int cols;                    // store: pages of L positions
+  int steps;                   // CTAs along the positions of one head (blockIdx.x = head * steps + step)
+  int* dev_err;
+};
+
+// Largest of the eight |x| of a vector of bf16, as the bits of its magnitude (a NaN's bits are
+// above infinity's, which are above every number's, so both come through).
+__device__ __forceinline__ uint32_t absmax_bits(uint4 v, uint32_t m) {
+  uint32_t a = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m, max(a & 0xffffu, a >> 16));
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The codes of eight bf16 under scale s: x / s as the definition has it, so an IEEE division
+// (exact ties between two codes exist in plenty: bf16 has few mantissas).
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(uint4 v, float s) {
+  if (s == 0.f) return make_uint2(0u, 0u);
+  uint2 r;
+  r.x = code2<FMT>(bf16_lo(v.x) / s, bf16_hi(v.x) / s) | (code2<FMT>(bf16_lo(v.y) / s, bf16_hi(v.y) / s) << 16);
+  r.y = code2<FMT>(bf16_lo(v.z) / s, bf16_hi(v.z) / s) | (code2<FMT>(bf16_lo(v.w) / s, bf16_hi(v.w) / s) << 16);
+  return r;
+}
+
+// Eight held codes under a grown scale: the nearest code to (code * s_old) / s.
+template <int FMT>
+__device__ __forceinline__ uint2 recode8(uint2 c, float s_old, float s) {
+  float x[4], y[4];
+  decode4<FMT>(c.x, x);
+  decode4<FMT>(c.y, y);
+  uint2 r;
+  r.x = code2<FMT>(x[0] * s_old / s, x[1] * s_old / s) | (code2<FMT>(x[2] * s_old / s, x[3] * s_old / s) << 16);
+  r.y = code2<FMT>(y[0] * s_old / s, y[1] * s_old / s) | (code2<FMT>(y[2] * s_old / s, y[3] * s_old / s) << 16);
+  return r;
+}
+
+// Largest of `m` over the group of `gt` threads (whole warps) that works on one page; every
+// thread of the CTA calls it. s_red holds a word for each warp.
+__device__ __forceinline__ uint32_t group_max(uint32_t m, int gt, uint32_t* s_red) {
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (gt == 32) return m;
+  __syncthreads();                       // the words of an earlier call have been read
+  if (lane_id() == 0) s_red[warp_id()] = m;
+  __syncthreads();
+  const int w0 = warp_id() / (gt / 32) * (gt / 32);
+  for (int w = 0; w < gt / 32; ++w) m = max(m, s_red[w0 + w]);
+  return m;
+}
+
+// ------------------------------------------------------------------ store
+// A group of page * d / 32 threads stores one page of one head; a CTA holds 256 threads or one
+// group. blockIdx.y: keys, values.
+template <int FMT>
+__global__ void __launch_bounds__(512) cache_store_kernel(const RowArgs a) {
+  __shared__ uint32_t s_red[16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int kv = blockIdx.y;
+  const int gt = a.page * a.d / 32;                     // threads of a group
+  const int per = blockDim.x / gt;
+  const int t = threadIdx.x % gt;
+  const int mbh = blockIdx.x / a.steps;
+  const int j = (blockIdx.x - mbh * a.steps) * per + threadIdx.x / gt;   // page of the sequence
+  const int cpr = a.d / 8;                              // vectors of a row
+  const int b = mbh / a.H % a.B;
+  int rows = 0, page = -1;                              // rows of this page that are stored
+  if (j < a.cols) {
+    rows = min(a.page, (a.lens ? min(a.lens[b], a.L) : a.L) - j * a.page);
+    if (rows > 0) page = checked_page(a.table, a.table_cols, b, j, a.n_pages, a.dev_err);
+    if (page < 0) rows = 0;
+  }
+  const uint4* src = a.X[kv] + (static_cast<long long>(mbh) * a.L + static_cast<long long>(j) * a.page) * cpr;
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = t + i * gt;
+    v[i] = c < rows * cpr ? __ldcs(src + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = absmax_bits(v[i], m);
+  m = group_max(m, gt, s_red);
+  if (rows <= 0) return;
+  const float s = __uint_as_float(m << 16) / CodeTop<FMT>::value;
+  const long long mat = mbh / (a.B * a.H);
+  const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;   // page and head
+  uint2* dst = a.code[kv] + ph * (a.page * cpr);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = t + i * gt;
+    if (c < rows * cpr) dst[c] = encode8<FMT>(v[i], s);
+  }
+  if (t == 0) a.scale[kv][ph] = s;
+}
+
+// ------------------------------------------------------------------ scatter_rows
+constexpr int kMaxCap = 4096;
+
+// The CTAs (x = split, y = (mat, b, h), z = keys/values) of one head share the pages that its
+// rows fall in: the first listed row of a page leads, leader number n goes to split n mod
+// gridDim.x. A page is then rebuilt as in the store, from the new rows and the held codes.
+template <int FMT>
+__global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
+  __shared__ uint32_t s_red[16];
+  __shared__ int s_col[kMaxCap];         // page column of each listed row, -1 = not written
+  __shared__ int s_src[128];             // row of the page -> listed row, -1 = none
+  __shared__ int s_lead[kMaxCap];        // the leaders of this CTA
+  __shared__ int s_nlead, s_count[16], s_base;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int kv = blockIdx.z;
+  const int mbh = blockIdx.y;
+  const int b = mbh / a.H % a.B;
+  const int n = max(0, min(a.n_rows[b], a.cap));
+  const int len = a.lens[b];
+  const int32_t* rows = a.rows + static_cast<size_t>(b) * a.cap;
+  const int cpr = a.d / 8, gt = blockDim.x, t = threadIdx.x;
+  bool sorted = true;
+  for (int i = t; i < n; i += gt) {
+    const int r = rows[i];
+    const bool ok = r >= 0 && r / a.page < a.table_cols;
+    if (!ok) record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
+    s_col[i] = ok ? r / a.page : -1;
+    sorted = sorted && ok && (i == 0 || rows[i - 1] < r);
+  }
+  if (t == 0) {
+    s_nlead = 0;
+    s_base = 0;
+  }
+  sorted = __syncthreads_and(sorted);
+  // leaders in the order of the list, numbered by a scan over chunks of the CTA
+  for (int i0 = 0; i0 < n; i0 += gt) {
+    const int i = i0 + t;
+    bool lead = i < n && s_col[i] >= 0;
+    if (lead && sorted) lead = i == 0 || s_col[i - 1] != s_col[i];
+    else if (lead)
+      for (int j = 0; j < i && lead; ++j) lead = s_col[j] != s_col[i];
+    const unsigned bal = __ballot_sync(0xffffffffu, lead);
+    if (lane_id() == 0) s_count[warp_id()] = __popc(bal);
+    __syncthreads();
+    int at = s_base;
+    for (int w = 0; w < warp_id(); ++w) at += s_count[w];
+    at += __popc(bal & ((1u << lane_id()) - 1u));
+    if (lead && at % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) s_lead[at / gridDim.x] = i;
+    __syncthreads();
+    if (t == 0) {
+      for (int w = 0; w < (gt + 31) / 32; ++w) s_base += s_count[w];
+      const int own = s_base - static_cast<int>(blockIdx.x);
+      s_nlead = own <= 0 ? 0 : (own + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    }
+    __syncthreads();
+  }
+  const int nlead = s_nlead;
+  const long long mat = mbh / (a.B * a.H);
+  for (int l = 0; l < nlead; ++l) {
+    const int first = s_lead[l], col = s_col[first];
+    __syncthreads();                     // the previous page's s_src has been read
+    for (int r = t; r < a.page; r += gt) {
+      // the last listed row of each position
+      int src = -1;
+      const int last = sorted ? min(n, first + a.page) : n;
+      for (int i = first; i < last; ++i)
+        if (s_col[i] == col && rows[i] - col * a.page == r) src = i;
+      s_src[r] = src;
+    }
+    const int page = checked_page(a.table, a.table_cols, b, col, a.n_pages, a.dev_err);
+    __syncthreads();
+    if (page < 0) continue;              // the same for the whole CTA
+    const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;
+    const bool held = col * a.page < len;
+    const float s_old = held ? a.scale[kv][ph] : 0.f;
+    uint4 v[4];
+    int src[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = t + i * gt;          // vector of the page: row c / cpr
+      src[i] = s_src[c / cpr];
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (src[i] >= 0) v[i] = __ldg(a.X[kv] + (static_cast<long long>(mbh) * a.cap + src[i]) * cpr + c % cpr);
+      m = absmax_bits(v[i], m);
+    }
+    m = group_max(m, gt, s_red);         // (its barriers also order the read of s_old before the write below)
+    const float s_new = __uint_as_float(m << 16) / CodeTop<FMT>::value;
+    const bool grown = !(s_new <= s_old) && s_old == s_old;      // a NaN stays what it is
+    const float s = grown ? s_new : s_old;
+    uint2* dst = a.code[kv] + ph * (a.page * cpr);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = t + i * gt;
+      if (src[i] >= 0) dst[c] = encode8<FMT>(v[i], s);
+      else if (held && grown && col * a.page + c / cpr < len) dst[c] = recode8<FMT>(dst[c], s_old, s);
+    }
+    __syncthreads();                     // every thread has read s_old
+    if (t == 0) a.scale[kv][ph] = s;
+  }
+}
+
+// ------------------------------------------------------------------ load
+// A CTA loads 8 KB of codes (64 rows of 128 or 128 rows of 64) of one head: two 16-byte vectors
+// a thread, so that 64 KB of reads are in flight on a full SM.
+constexpr int kLoadThreads = 256;
+template <int FMT>
+__global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const RowArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int kv = blockIdx.y;
+  const int mbh = blockIdx.x / a.steps, step = blockIdx.x - mbh * a.steps;
+  const int b = mbh / a.H % a.B;
+  const int cpr = a.d / 16;                                      // code vectors of a row
+  const int rows_cta = kLoadThreads * 2 / cpr;
+  const int n = min(a.L, a.lens[b] - a.start);                   // rows of this sequence
+  const long long mat = mbh / (a.B * a.H);
+  uint4 c[2];
+  float s[2];
+  int row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = threadIdx.x + i * kLoadThreads;
+    row[i] = step * rows_cta + x / cpr;
+    c[i] = make_uint4(0u, 0u, 0u, 0u);
+    s[i] = 0.f;
+    if (row[i] < n) {
+      const int pos = a.start + row[i];
+      const int page = checked_page(a.table, a.table_cols, b, pos / a.page, a.n_pages, a.dev_err);
+      if (page >= 0) {
+        const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;
+        c[i] = __ldcs(reinterpret_cast<const uint4*>(a.code[kv]) + (ph * a.page + pos % a.page) * cpr + x % cpr);
+        s[i] = a.scale[kv][ph];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (row[i] >= n) continue;
+    const int x = threadIdx.x + i * kLoadThreads;
+    uint32_t w[8];
+    const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[4];
+      decode4<FMT>(in[j], f);
+      w[2 * j] = pack_bf16x2(f[0] * s[i], f[1] * s[i]);
+      w[2 * j + 1] = pack_bf16x2(f[2] * s[i], f[3] * s[i]);
+    }
+    uint4* dst = a.out[kv] + ((static_cast<long long>(mbh) * a.L + row[i]) * cpr + x % cpr) * 2;
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// ------------------------------------------------------------------ copy of pages
+// The page of one layer is Hkv * page * d contiguous codes, keys and values alike. A CTA copies
+// 16 KB pieces (four vectors a thread in flight); the last piece number of a page stands for
+// its scales. How many pairs there are is known on the device only, so a grid that fills the
+// GPU walks over them.
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(uint4* k, uint4* v, float* ks, float* vs, int n_mat,
+                                                                  int n_pages, int H, long long page_vecs,
+                                                                  const int32_t* pairs, const int32_t* n_pairs,
+                                                                  int pair_cap, int* dev_err) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = max(0, min(*n_pairs, pair_cap));
+  const int pieces = static_cast<int>((page_vecs + 4 * kCopyThreads - 1) / (4 * kCopyThreads));
+  const int per_page = 2 * pieces + 1;
+  const int total = per_page * n * n_mat;
+  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+    const int pm = w / per_page, piece = w - pm * per_page;
+    const int r = pm / n_mat, m = pm - r * n_mat;
+    const int src = pairs[2 * r], dst = pairs[2 * r + 1];
+    if (src < 0 || src >= n_pages || dst < 0 || dst >= n_pages) {
+      if (threadIdx.x == 0) record_dev_error(dev_err, DEV_ERR_BAD_INDEX);
+      continue;
+    }
+    const long long so = static_cast<long long>(m) * n_pages + src, dn = static_cast<long long>(m) * n_pages + dst;
+    if (piece == 2 * pieces) {
+      for (int h = threadIdx.x; h < H; h += kCopyThreads) {
+        ks[dn * H + h] = ks[so * H + h];
+        vs[dn * H + h] = vs[so * H + h];
+      }
+      continue;
+    }
+    uint4* base = piece < pieces ? k : v;
+    const long long off = static_cast<long long>(piece < pieces ? piece : piece - pieces) * (4 * kCopyThreads) + threadIdx.x;
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (off + i * kCopyThreads < page_vecs) x[i] = __ldcs(base + so * page_vecs + off + i * kCopyThreads);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (off + i * kCopyThreads < page_vecs) base[dn * page_vecs + off + i * kCopyThreads] = x[i];
+  }
+}
+
+RowArgs row_args(const focus_cache* c, const int32_t* table, int table_cols, const int32_t* lens, int B) {
+  RowArgs a{};
+  a.code[0] = static_cast<uint2*>(c->k);
+  a.code[1] = static_cast<uint2*>(c->v);
+  a.scale[0] = c->k_scale;
+  a.scale[1] = c->v_scale;
+  a.lens = lens;
+  a.table = table;
+  a.table_cols = table_cols;
+  a.B = B;
+  a.H = c->Hkv;
+  a.d = c->d;
+  a.page = c->page;
+  a.n_pages = c->n_pages;
+  a.dev_err = device_error_word();
+  return a;
+}
+
+int launched(cudaError_t e, const char* what) {
+  note_launch();
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_error("%s launch: %s", what, cudaGetErrorString(e));
+    return FOCUS_ERR_CUDA;
+  }
+  return FOCUS_OK;
+}
+
+}  // namespace
+
+}  // namespace focus
+
+using namespace focus;
+
+extern "C" int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B, int L, const int32_t* lens,
+                                 const int32_t* table, int table_cols, const focus_cache* cache, void* stream) {
+  FOCUS_CHECK_ARG(K && V, "null pointer argument");
+  if (const int st = check_cache(cache, table, table_cols, false)) return st;
+  FOCUS_CHECK_ARG(B >= 0 && L >= 1, "bad sizes (B=%d L=%d)", B, L);
+  FOCUS_CHECK_ARG(aligned16(K) && aligned16(V), "tensors must be 16-byte aligned");
+  RowArgs a = row_args(cache, table, table_cols, lens, B);
+  a.X[0] = reinterpret_cast<const uint4*>(K);
+  a.X[1] = reinterpret_cast<const uint4*>(V);
+  a.L = L;
+  a.cols = (L + a.page - 1) / a.page;
+  const int gt = a.page * a.d / 32, threads = std::max(256, gt), per = threads / gt;
+  a.steps = (a.cols + per - 1) / per;
+  const long long blocks = static_cast<long long>(cache->n_mat) * B * a.H * a.steps;
+  if (blocks == 0) return FOCUS_OK;
+  FOCUS_CHECK_ARG(blocks < (1LL << 31), "too large");
+  auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_store_kernel<FOCUS_CACHE_E4M3> : cache_store_kernel<FOCUS_CACHE_INT8>;
+  return launched(launch_k(kern, dim3(static_cast<unsigned>(blocks), 2), dim3(threads), 0,
+                           static_cast<cudaStream_t>(stream), a),
+                  "cache_store");
+}
+
+extern "C" int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf16* V_rows, const int32_t* rows,
+                                        const int32_t* n_rows, int B, int cap, const int32_t* lens,
+                                        const int32_t* table, int table_cols, const focus_cache* cache, void* stream) {
+  FOCUS_CHECK_ARG(K_rows && V_rows && rows && n_rows && lens, "null pointer argument");
+  if (const int st = check_cache(cache, table, table_cols, false)) return st;
+  FOCUS_CHECK_ARG(B >= 0 && cap >= 1, "bad sizes (B=%d cap=%d)", B, cap);
+  if (cap > kMaxCap) {
+    set_error("cache_scatter_rows: cap %d exceeds %d", cap, kMaxCap);
+    return FOCUS_ERR_UNSUPPORTED;
+  }
+  FOCUS_CHECK_ARG(aligned16(K_rows) && aligned16(V_rows), "tensors must be 16-byte aligned");
+  const long long units = static_cast<long long>(cache->n_mat) * B * cache->Hkv;
+  if (units == 0) return FOCUS_OK;
+  if (units > 65535) {
+    set_error("cache_scatter_rows: n_mat * B * Hkv = %lld exceeds 65535", units);
+    return FOCUS_ERR_UNSUPPORTED;
+  }
+  RowArgs a = row_args(cache, table, table_cols, lens, B);
+  a.X[0] = reinterpret_cast<const uint4*>(K_rows);
+  a.X[1] = reinterpret_cast<const uint4*>(V_rows);
+  a.rows = rows;
+  a.n_rows = n_rows;
+  a.cap = cap;
+  // rows next to each other fall in cap / page + 1 pages or fewer
+  const int splits = std::min(16, (cap + a.page - 1) / a.page + 1);
+  auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3>
+                                                : cache_scatter_kernel<FOCUS_CACHE_INT8>;
+  return launched(launch_k(kern, dim3(splits, static_cast<unsigned>(units), 2), dim3(a.page * a.d / 32), 0,
+                           static_cast<cudaStream_t>(stream), a),
+                  "cache_scatter_rows");
+}
+
+extern "C" int focus_cache_load(const focus_cache* cache, const int32_t* table, int table_cols, const int32_t* lens,
+                                int B, int start, int L, focus_bf16* K, focus_bf16* V, void* stream) {
+  FOCUS_CHECK_ARG(K && V && lens, "null pointer argument");
+  if (const int st = check_cache(cache, table, table_cols, false)) return st;
+  FOCUS_CHECK_ARG(B >= 0 && L >= 1 && start >= 0 && static_cast<long long>(start) + L < (1LL << 31),
+                  "bad sizes (B=%d start=%d L=%d)", B, start, L);
+  FOCUS_CHECK_ARG(aligned16(K) && aligned16(V), "tensors must be 16-byte aligned");
+  RowArgs a = row_args(cache, table, table_cols, lens, B);
+  a.out[0] = reinterpret_cast<uint4*>(K);
+  a.out[1] = reinterpret_cast<uint4*>(V);
+  a.start = start;
+  a.L = L;
+  const int rows_cta = kLoadThreads * 2 / (a.d / 16);
+  a.steps = (L + rows_cta - 1) / rows_cta;
+  const long long blocks = static_cast<long long>(cache->n_mat) * B * a.H * a.steps;
+  if (blocks == 0) return FOCUS_OK;
+  FOCUS_CHECK_ARG(blocks < (1LL << 31), "too large");
+  auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_load_kernel<FOCUS_CACHE_E4M3> : cache_load_kernel<FOCUS_CACHE_INT8>;
+  return launched(launch_k(kern, dim3(static_cast<unsigned>(blocks), 2), dim3(kLoadThreads), 0,
+                           static_cast<cudaStream_t>(stream), a),
+                  "cache_load");
+}
+
+extern "C" int focus_pages_copy(const focus_cache* cache, const int32_t* pairs, const int32_t* n_pairs, int pair_cap,
+                                void* stream) {
+  FOCUS_CHECK_ARG(pairs && n_pairs && pair_cap >= 0, "null pointer argument");
+  if (const int st = check_cache(cache, pairs, 2, false)) return st;
+  if (cache->n_mat == 0 || pair_cap == 0) return FOCUS_OK;
+  const long long page_vecs = static_cast<long long>(cache->Hkv) * cache->page * cache->d / 16;
+  const long long most = static_cast<long long>(pair_cap) * cache->n_mat * (2 * ((page_vecs + 1023) / 1024) + 1);
+  if (most >= (1LL << 31)) {
+    set_error("pages_copy: %d pairs of %d layers are too many for one call", pair_cap, cache->n_mat);
+    return FOCUS_ERR_UNSUPPORTED;
+  }
+  const long long grid = std::min<long long>(most, static_cast<long long>(device_sm_count()) * 8);
+  return launched(launch_k(pages_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kCopyThreads), 0,
+                           static_cast<cudaStream_t>(stream), static_cast<uint4*>(cache->k),
+                           static_cast<uint4*>(cache->v), cache->k_scale, cache->v_scale, cache->n_mat, cache->n_pages,
+                           cache->Hkv, page_vecs, pairs, n_pairs, pair_cap, device_error_word()),
+                  "pages_copy");
+}

@@ -267,6 +267,157 @@ FOCUS_API int focus_sparse_attention_noalloc(const focus_bf16* Q_active, const i
                                              int Hq, int Hkv, int L, int d, int acap, float scale,
                                              focus_bf16* O_active, void* stream);
 
+/*
+ * ---------------------------------------------------------------- 8-bit paged cache
+ * The approximate KV cache (Focus-dLLM summary page, "近似KV缓存") held in 8 bits, in pages of
+ * `page` positions that sequences can share. The pages describe a cache of the model's own
+ * type only; this form halves the bytes that every attention of a step reads.
+ *
+ * Codes k, v [n_mat, n_pages, Hkv, page, d] (n_mat layers) with one fp32 scale for each
+ * layer, page and head, k_scale, v_scale [n_mat, n_pages, Hkv]: an element stands for
+ * code * scale. format FOCUS_CACHE_E4M3 (e4m3 floats, top = 448) or FOCUS_CACHE_INT8
+ * (two's complement, top = 127). A page's scale is s = max|x| / top over the rows written to
+ * it, a code the nearest (ties to even) to x / s, both divisions rounded in fp32; s = 0 (a
+ * page of zeros) gives codes 0. Values must be finite: a NaN or an infinity makes the scale
+ * of its page and head NaN or infinite, and what reads that page NaN.
+ *
+ * table [B, table_cols] int32 (device): page table[b, j] holds the positions
+ * [j * page, (j + 1) * page) of sequence b. Entries that a call needs must lie in
+ * [0, n_pages); a position whose entry does not is skipped (not written; not attended;
+ * loaded as zeros) and flagged in the device error word (code 5), as are positions behind
+ * table_cols * page. A page that a call writes must be named once among the sequences of
+ * that call (focus_pages_own gives a sequence its own copies of shared pages).
+ *
+ * Requires d in {64, 128}, page in {16, 32, 64, 128}, Hkv >= 1, n_pages * Hkv < 2^31,
+ * k, v 16-byte aligned, scales 4-byte aligned. The struct lives on the host and is read
+ * during the call only; a layer's cache is the struct with its four pointers moved to that
+ * layer and n_mat = 1.
+ */
+typedef enum { FOCUS_CACHE_E4M3 = 0, FOCUS_CACHE_INT8 = 1 } focus_cache_format;
+
+typedef struct {
+  void* k;          /* codes [n_mat, n_pages, Hkv, page, d] */
+  void* v;
+  float* k_scale;   /* [n_mat, n_pages, Hkv] */
+  float* v_scale;
+  int n_mat, n_pages, Hkv, page, d;
+  int format;       /* focus_cache_format */
+} focus_cache;
+
+/*
+ * Block entry: the keys and values of positions [0, lens[b]) go into the cache, their pages'
+ * scales are set anew. K, V [n_mat, B, Hkv, L, d] bf16; lens [B] int32 (device, clamped to
+ * [0, L]) or NULL for L. Positions behind lens[b] keep their codes (in the last page, under
+ * that page's new scale). One pass: every element is read once and every code written once.
+ */
+FOCUS_API int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B, int L, const int32_t* lens,
+                                const int32_t* table, int table_cols, const focus_cache* cache, void* stream);
+
+/*
+ * The refresh of single rows (as focus_scatter_rows): position rows[b, i] of sequence b takes
+ * K_rows[m, b, h, i], V_rows[m, b, h, i] for i < n_rows[b]; K_rows, V_rows
+ * [n_mat, B, Hkv, cap, d] bf16, rows [B, cap], n_rows [B] int32 (device), in any order; of a
+ * position listed twice the later row stays. lens [B] int32 (device): positions the sequence
+ * held before the call. The scale of a page that held any only grows: s' = max(s, max|new| /
+ * top); when it does, its other held rows are coded again, the nearest code to
+ * (code * s) / s' (product and quotient rounded in fp32). A page that starts at or behind
+ * lens[b] held nothing: s' = max|new| / top. Other positions behind lens[b] keep their codes.
+ * Negative rows are flagged like positions behind the table. Requires 1 <= cap <= 4096.
+ */
+FOCUS_API int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf16* V_rows, const int32_t* rows,
+                                       const int32_t* n_rows, int B, int cap, const int32_t* lens,
+                                       const int32_t* table, int table_cols, const focus_cache* cache, void* stream);
+
+/*
+ * Positions [start, min(start + L, lens[b])) of the cache as bf16: K[m, b, h, i] = code * scale
+ * of position start + i, rounded once; K, V [n_mat, B, Hkv, L, d]. Rows behind lens[b] are left
+ * as they were. start >= 0; lens as in focus_cache_store, but not clamped to L.
+ */
+FOCUS_API int focus_cache_load(const focus_cache* cache, const int32_t* table, int table_cols, const int32_t* lens,
+                               int B, int start, int L, focus_bf16* K, focus_bf16* V, void* stream);
+
+/*
+ * (3) Dense attention from the cache (as focus_dense_attention): for i < n_q[b] (all qcap rows
+ * when n_q == NULL) of query head hq, O[b, hq, i] = softmax over positions j < lens[b] of
+ * scale * q_i . k_j, applied to V, with k_j, v_j the values that the codes stand for. Rows
+ * i >= n_q[b], and every row of a sequence with lens[b] <= 0, are written as zero. Q, O
+ * [B, Hq, qcap, d] bf16; cache of one layer (n_mat = 1); lens [B] int32 (device).
+ * ws/ws_bytes: at least focus_cache_workspace_bytes(...) bytes, 256-byte aligned; two calls
+ * that may overlap on the GPU need a workspace each. Requires Hq % Hkv == 0, qcap >= 1.
+ */
+FOCUS_API int focus_cache_attention(const focus_bf16* Q, const int32_t* n_q, const focus_cache* cache,
+                                    const int32_t* table, int table_cols, const int32_t* lens, int B, int Hq,
+                                    int qcap, float scale, focus_bf16* O, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * (5) Sparse attention from the cache (as focus_sparse_attention, each sequence with a prompt
+ * length of its own): the key set of (b, h) is sinks[b, h, :] U (blocks [j * page,
+ * min(P[b], (j + 1) * page)) for j in blocks[b, h, :]) U [g0[b], g0[b] + G), taken as a SET.
+ * P, g0 [B] int32 (device), 0 <= P[b] <= g0[b]; sinks [B, Hkv, S] (NULL when S = 0) and
+ * blocks [B, Hkv, C] int32 (device), negative entries ignored, repeated entries counted once,
+ * in any order. Requires G >= 1, 0 <= S <= 1024, 1 <= C <= 1024; the rest as above.
+ */
+FOCUS_API int focus_cache_sparse_attention(const focus_bf16* Q_active, const int32_t* n_active,
+                                           const focus_cache* cache, const int32_t* table, int table_cols,
+                                           const int32_t* P, const int32_t* g0, int G, const int32_t* sinks, int S,
+                                           const int32_t* blocks, int C, int B, int Hq, int qcap, float scale,
+                                           focus_bf16* O_active, void* ws, size_t ws_bytes, void* stream);
+
+FOCUS_API size_t focus_cache_workspace_bytes(int B, int Hq, int Hkv, int d, int qcap);
+
+/*
+ * Pages of the cache. refs [n_pages]: table entries that name the page, 0 = free;
+ * table [n_seq, table_cols]: -1 behind held[s]; held [n_seq]: pages of sequence s (all int32,
+ * device). Every call runs on the device without a host round trip (it can be captured);
+ * calls on the same pages must be ordered (one stream, or events). Free pages are taken in
+ * ascending order, for the listed sequences in the order of the list, so results do not
+ * depend on timing. status [1] int32 (device): 0, or the number of pages (or pairs) that are
+ * missing; a call that is short of any changes nothing else. Lists hold n <= 1024 entries
+ * (n = 0 does nothing). List entries that name no sequence, and table entries that name no
+ * page, are skipped and flagged in the device error word (code 5).
+ */
+typedef struct {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* held;
+  int n_pages, n_seq, table_cols;
+} focus_pages;
+
+/* Sequences seqs[i] grow to want[i] pages (shorter wants change nothing; a want above
+ * table_cols is skipped and flagged). */
+FOCUS_API int focus_pages_reserve(const focus_pages* pages, const int32_t* seqs, const int32_t* want, int n,
+                                  int32_t* status, void* stream);
+
+/* Sequence dst[i], which holds nothing (else skipped and flagged), shares the first
+ * min(keep[i], held) pages of src[i]; in the order of the list. Nothing is copied. */
+FOCUS_API int focus_pages_fork(const focus_pages* pages, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                               int n, void* stream);
+
+/* Copy on write: pages first[i] <= j < last[i] of sequence seqs[i] that others share are
+ * replaced by free pages; pairs[r] = (shared page, own page), r < n_pairs[0], is what
+ * focus_pages_copy has to copy. Of a page that every one of its sequences is listed with,
+ * the last in the list keeps it. pairs [pair_cap, 2], n_pairs [1]. */
+FOCUS_API int focus_pages_own(const focus_pages* pages, const int32_t* seqs, const int32_t* first,
+                              const int32_t* last, int n, int32_t* pairs, int pair_cap, int32_t* n_pairs,
+                              int32_t* status, void* stream);
+
+/* Sequences seqs[i] give up their pages behind the first keep[i] (0: all of them). */
+FOCUS_API int focus_pages_release(const focus_pages* pages, const int32_t* seqs, const int32_t* keep, int n,
+                                  void* stream);
+
+/* The n live pages move to [0, n): the live pages at or behind n, ascending, into the free
+ * ones before n, ascending. pairs [pair_cap, 2] and n_pairs [1] are what focus_pages_copy has
+ * to copy; remap [n_pages] = each page's new index, -1 for free ones. refs and the first held
+ * entries of the tables follow. pair_cap >= n_pages / 2 (else FOCUS_ERR_CAPACITY). */
+FOCUS_API int focus_pages_compact(const focus_pages* pages, int32_t* pairs, int pair_cap, int32_t* n_pairs,
+                                  int32_t* remap, void* stream);
+
+/* Codes and scales of page pairs[r, 0] to page pairs[r, 1], r < min(n_pairs[0], pair_cap), in
+ * all n_mat layers. No page may be both source and target, or target twice. Pairs outside
+ * [0, n_pages) are skipped and flagged. */
+FOCUS_API int focus_pages_copy(const focus_cache* cache, const int32_t* pairs, const int32_t* n_pairs, int pair_cap,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif
