@@ -13,8 +13,10 @@
 // The keys of a tile of 128 are the M side, the queries the N side (swap-AB):
 //   S^T[key, q] = K_tile . Q^T        (M = 128 keys, N = queries, K = d)
 //   O^T[dim, q] = V_tile^T . P^T      (M = d,        N = queries, K = 128 keys)
-// e4m3 products of hi and lo add up in one fp32 accumulator; int8 products land in two int32
-// accumulators side by side. V_tile^T is the row-major tile read as an MN-major A operand.
+// hi and lo stand side by side in N, so a product of both is one MMA and their sums are added
+// when they are read (as two MMAs into one accumulator, which e4m3 could do, a tile took 1550
+// cycles of MMA instead of half that: at these widths an MMA costs about 100 cycles whatever
+// its N). V_tile^T is the row-major tile and P^T the rows of a key each, both MN-major.
 //
 // Scales: a key's scale multiplies its row of S^T (a thread owns a key). A value's scale goes
 // into P, relative to the largest of the tile, and that largest into the sum of O over tiles,
@@ -136,7 +138,7 @@ struct Desc {               // a run of tiles of one unit that this CTA works on
 template <int NQ, int STAGES>
 struct __align__(16) Book {
   uint64_t full[STAGES], empty[STAGES];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[4], p_full[2], o_full[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t d_full[kDescs], d_empty[kDescs];
   uint64_t x_full, x_done, drain;
@@ -151,9 +153,8 @@ struct __align__(16) Book {
   float q_scale[2][NQ];
   float red[2][2][4][32];               // [group][parity][warp][column]
   alignas(16) float2 pre[8][32];        // [warp][column]: (query scale, -reference)
-  alignas(16) float al[8][32];          // [warp][column]: factor of the held row sum
-  alignas(16) float be[8][32];          // factor of the new one
-  alignas(16) float2 post[8][2][32];    // [warp][buffer][column]: factors of the held and of the new O
+  alignas(16) float be[8][32];          // [warp][column]: factor of the tile's row sum
+  alignas(16) float post[8][2][32];     // [warp][buffer][column]: factor of the tile's O
   alignas(16) float2 xml[2][32];        // (m, l) of the other group's columns
   int blk[kMaxList], snk[kMaxList];
 };
@@ -165,12 +166,14 @@ struct Lay {
   static constexpr uint32_t kQ = kStages * 2 * kTile;              // 2 buffers of hi, lo rows
   static constexpr uint32_t kQBuf = 2 * NQ * D;
   static constexpr uint32_t kP = kQ + 2 * kQBuf;
-  static constexpr uint32_t kPBuf = 2 * NQ * 128;
+  static constexpr uint32_t kPRow = 2 * NQ;                        // bytes of a key's row of P: hi, lo
+  static constexpr uint32_t kPBuf = 128 * kPRow;
   static constexpr uint32_t kBook = kP + 2 * kPBuf;
   static constexpr uint32_t kBytes = kBook + sizeof(Book<NQ, kStages>) + 1024;
-  static constexpr int kAcc = FMT == FOCUS_CACHE_INT8 ? 2 * NQ : NQ;   // accumulator columns of a product
-  static constexpr uint32_t kTmemUsed = 4 * kAcc;
-  static constexpr uint32_t kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static constexpr int kAcc = 2 * NQ;                              // accumulator columns of a product: hi, lo
+  static constexpr int kS = NQ == 64 ? 2 : 4;                      // buffers of S^T
+  static constexpr uint32_t kTmemUsed = (kS + 2) * kAcc;
+  static constexpr uint32_t kTmem = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
   static_assert(kTmemUsed <= 512, "exceeds tensor memory");
   using Bk = Book<NQ, kStages>;
@@ -178,30 +181,33 @@ struct Lay {
 };
 
 // ------------------------------------------------------------------ small pieces
-// Byte offset of 16-byte chunk c of row r of a tile whose rows are D bytes, in the 128-byte
-// (D = 128) or 64-byte (D = 64) swizzle that the copies and the tensor cores use.
-template <int D>
+// Byte offset of 16-byte chunk c of row r of a tile whose rows are W bytes, in the swizzle of
+// that width (128, 64 or 32 bytes) that the copies and the tensor cores use: bits 4 and up of
+// the address are combined with bits 7 and up.
+template <int W>
 __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
-  return D == 128 ? static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4))
-                  : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  static_assert(W == 128 || W == 64 || W == 32, "row width");
+  const int x = W == 128 ? (r & 7) : W == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+  return static_cast<uint32_t>(r * W + ((c ^ x) << 4));
 }
 
-// Matrix descriptor of such a tile (8-row groups every 8 * D bytes). For the MN-major read of
-// V with D = 64, M = 128 needs two 64-wide columns of atoms: a leading stride of 0 reads the
-// one there is twice (dims 64 .. 127 of O^T repeat 0 .. 63 and are not used).
-template <int D>
+// Matrix descriptor of such a tile (8-row groups every 8 * W bytes), for a K-major operand whose
+// K is the row's bytes and for an MN-major one whose K is the rows. For the MN-major read of V
+// with d = 64, M = 128 needs two 64-wide columns of atoms: a leading stride of 0 reads the one
+// there is twice (dims 64 .. 127 of O^T repeat 0 .. 63 and are not used).
+template <int W>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
-  const uint64_t layout = D == 128 ? 2ull : 4ull;      // SWIZZLE_128B, SWIZZLE_64B
-  const uint64_t leading = D == 128 ? 1ull : 0ull;     // not used where one column of atoms is all there is
+  const uint64_t layout = W == 128 ? 2ull : W == 64 ? 4ull : 6ull;   // SWIZZLE_128B, _64B, _32B
+  const uint64_t leading = W == 128 ? 1ull : 0ull;     // not used where one column of atoms is all there is
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (leading << 16) |
-         (static_cast<uint64_t>((8 * D) >> 4) << 32) | (1ull << 46) | (layout << 61);
+         (static_cast<uint64_t>((8 * W) >> 4) << 32) | (1ull << 46) | (layout << 61);
 }
 
 template <int FMT>
-__device__ constexpr uint32_t idesc8(int N, bool a_mn_major) {
+__device__ constexpr uint32_t idesc8(int N, bool mn_major) {
   // D format (1 = f32, 2 = s32) | A, B format (e4m3 = 0 of kind::f8f6f4, s8 = 1 of kind::i8)
   const uint32_t d = FMT == FOCUS_CACHE_E4M3 ? 1u : 2u, f = FMT == FOCUS_CACHE_E4M3 ? 0u : 1u;
-  return (d << 4) | (f << 7) | (f << 10) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+  return (d << 4) | (f << 7) | (f << 10) | ((mn_major ? 3u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (128u >> 4 << 24);
 }
 
@@ -237,6 +243,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 1 in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e;
+}
+
+// n arrivals at once.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // Whether phase `parity` is over, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -250,23 +272,43 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// hi + lo of two probabilities (times 256 for e4m3, 16256 for int8): bytes of column 0 in bits
-// 0-7, of column 1 in bits 8-15.
+// hi and lo of four probabilities p times f (256 for e4m3, 16256 for int8, times the value's
+// relative scale), a byte each, column 0 lowest.
 template <int FMT>
-__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split4(const float (&p)[4], float f, uint32_t& hi, uint32_t& lo) {
   if constexpr (FMT == FOCUS_CACHE_E4M3) {
-    // in half precision: 11 bits hold p to 2^-12, and p - hi is exact
-    const __half2 p = __floats2half2_rn(p0, p1);
-    const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
-    const __half2 r = __hsub2(p, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-    hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // in half precision: 11 bits hold p to 2^-12, and p - hi is exact
+      const __half2 x = __floats2half2_rn(p[2 * i] * f, p[2 * i + 1] * f);
+      h[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+      const __half2 r = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3)));
+      l[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+    }
+    hi = __byte_perm(h[0], h[1], 0x5410);
+    lo = __byte_perm(l[0], l[1], 0x5410);
   } else {
-    const int a = __float2int_rn(p0), b = __float2int_rn(p1);
-    const int ah = (a + 64) >> 7, bh = (b + 64) >> 7;
-    hi = static_cast<uint32_t>(ah & 0xff) | (static_cast<uint32_t>(bh & 0xff) << 8);
-    lo = static_cast<uint32_t>((a - (ah << 7)) & 0xff) | (static_cast<uint32_t>((b - (bh << 7)) & 0xff) << 8);
+    // v = round(p f) + 64 by adding 1.5 * 2^23 + 64: v = 128 hi + (lo + 64) with lo + 64 in
+    // [0, 128), in the low 15 bits of the sum
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __float_as_uint(fmaf(p[2 * i], f, 12582976.f)), b = __float_as_uint(fmaf(p[2 * i + 1], f, 12582976.f));
+      const uint32_t w = __byte_perm(a, b, 0x5410);
+      h[i] = (w >> 7) & 0x00ff00ffu;
+      l[i] = (w & 0x007f007fu) + 0x00c000c0u;      // lo mod 256 in bits 0-7 and 16-23
+    }
+    hi = __byte_perm(h[0], h[1], 0x6420);
+    lo = __byte_perm(l[0], l[1], 0x6420);
   }
+}
+
+// The product of hi and lo from their accumulators.
+template <int FMT>
+__device__ __forceinline__ float both(uint32_t hi, uint32_t lo) {
+  if constexpr (FMT == FOCUS_CACHE_E4M3) return __uint_as_float(hi) + __uint_as_float(lo);
+  else return static_cast<float>(static_cast<int>(hi) * 128 + static_cast<int>(lo));
 }
 
 template <int FMT>
@@ -274,11 +316,88 @@ constexpr float prob_top() {
   return FMT == FOCUS_CACHE_E4M3 ? 256.f : 16256.f;
 }
 
+// Query q of the slice (head kvh * g + r / qcap, row r % qcap of r = row0 + q) as hi and lo rows
+// of the K-major B operand: a warp, rows first, first + step, ...
+template <int FMT, int D, int NQ>
+__device__ __noinline__ void split_queries(const CacheAttnArgs& a, const Desc& d, uint8_t* dst, float* q_scale, int first,
+                                           int step) {
+  constexpr int E = D / 32;                  // elements of a lane
+  constexpr int UN = 4;                      // rows in flight
+  const int lane = lane_id();
+  for (int q0 = first; q0 < NQ; q0 += step * UN) {
+    float x[UN][E];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int q = q0 + step * i, r = d.row0 + q;
+      const int qh = r / a.qcap, qi = r - qh * a.qcap;
+      const bool real = q < d.rows && qi < d.nq;
+      const __nv_bfloat16* src = a.Q + ((static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        uint32_t w = 0u;
+        if (real) w = __ldg(reinterpret_cast<const uint32_t*>(src) + e / 2);
+        x[i][e] = __uint_as_float(w << 16);
+        x[i][e + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int q = q0 + step * i;
+      if (q >= NQ) break;
+      float m = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        m = fmaxf(m, fabsf(x[i][e]));
+        bad |= !(fabsf(x[i][e]) <= 3.4e38f);
+      }
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      bad = __any_sync(0xffffffffu, bad);
+      float back;                            // what a unit of the row's codes stands for
+      uint32_t hi = 0, lo = 0;
+      if constexpr (FMT == FOCUS_CACHE_E4M3) {
+        // power of two that brings the largest element into [128, 256), from its exponent bits
+        const int ex = m > 0.f ? max(-120, min(120, 7 - (static_cast<int>(__float_as_uint(m) >> 23) - 127))) : 0;
+        const float up = __int_as_float((127 + ex) << 23);
+        back = __int_as_float((127 - ex) << 23);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float y0 = (a.negative ? -x[i][e] : x[i][e]) * up, y1 = (a.negative ? -x[i][e + 1] : x[i][e + 1]) * up;
+          const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+          const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+          hi |= static_cast<uint32_t>(h) << (8 * e);
+          lo |= static_cast<uint32_t>(
+                    __nv_cvt_float2_to_fp8x2(make_float2(y0 - hf.x, y1 - hf.y), __NV_SATFINITE, __NV_E4M3))
+                << (8 * e);
+        }
+      } else {
+        const float up = m > 1e-30f ? 16256.f / m : 0.f;
+        back = m > 1e-30f ? m / 16256.f : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int v = __float2int_rn((a.negative ? -x[i][e] : x[i][e]) * up), vh = (v + 64) >> 7;
+          hi |= static_cast<uint32_t>(vh & 0xff) << (8 * e);
+          lo |= static_cast<uint32_t>((v - (vh << 7)) & 0xff) << (8 * e);
+        }
+      }
+      const uint32_t at = row_chunk<D>(q, lane * E / 16) + (lane * E & 15);
+      if constexpr (E == 4) {
+        *reinterpret_cast<uint32_t*>(dst + at) = hi;
+        *reinterpret_cast<uint32_t*>(dst + NQ * D + at) = lo;
+      } else {
+        *reinterpret_cast<uint16_t*>(dst + at) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t*>(dst + NQ * D + at) = static_cast<uint16_t>(lo);
+      }
+      if (lane == 0) q_scale[q] = bad ? NAN : back * a.scale_log2;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 template <int FMT, int D, int NQ, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const CacheAttnArgs a) {
+                      const __grid_constant__ CacheAttnArgs a) {
   using SM = Lay<FMT, D, NQ>;
   constexpr int STAGES = SM::kStages;
   constexpr bool kBoth = NQ == 64;               // both groups work on every tile
@@ -294,11 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk->full[i], 2);                // the copies' bytes, the keys' scales
       mbar_init(&bk->empty[i], 1);
     }
+    for (int i = 0; i < SM::kS; ++i) mbar_init(&bk->s_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bk->s_full[i], 1);
       mbar_init(&bk->p_full[i], kBoth ? 8 : 4);
       mbar_init(&bk->o_full[i], 1);
-      mbar_init(&bk->q_full[i], 2);
+      mbar_init(&bk->q_full[i], 10);             // the query and the softmax warps
       mbar_init(&bk->q_empty[i], 9);             // the last QK, and the softmax warps that read the scales
     }
     for (int i = 0; i < kDescs; ++i) {
@@ -323,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t tmem = bk->tmem_base;
-  const uint32_t tS = tmem, tO = tmem + 2 * SM::kAcc;
+  const uint32_t tS = tmem, tO = tmem + SM::kS * SM::kAcc;
 
   if (warp == kProducer) {
     // ------------------------------------------------------------ producer
@@ -645,75 +764,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr int kQK = FMT == FOCUS_CACHE_E4M3 ? NQ : 2 * NQ;      // N of the products
-      const uint32_t id_qk = idesc8<FMT>(kQK, false), id_pv = idesc8<FMT>(kQK, true);
-      const uint64_t k0 = tile_desc<D>(smem_u32(smem));
-      const uint64_t q0 = tile_desc<D>(smem_u32(smem) + SM::kQ);
-      const uint64_t p0 = tile_desc<128>(smem_u32(smem) + SM::kP);
-      bool ok = true, more = true;
-      int di = 0, left = 0, j_qk = 0;      // descriptor, tiles left in it, next tile of QK
-      // QK of the next tile, over the ends of the runs; false at the end
-      auto issue_qk = [&]() -> bool {
-        bool first = false;
-        if (left == 0) {
-          if (di > 0) mbar_arrive(&bk->d_empty[(di - 1) % kDescs]);
-          if (!mbar_wait(&bk->d_full[di % kDescs], (di / kDescs) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA)) {
-            ok = false;
-            return false;
-          }
-          left = bk->desc[di % kDescs].n;
-          if (left == 0) return false;
-          ++di;
-          first = true;
-        }
-        const int qb = (di - 1) & 1, s = j_qk % STAGES, buf = j_qk & 1;
-        if (first)
-          ok = mbar_wait(&bk->q_full[qb], ((di - 1) >> 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA);
-        ok = ok && mbar_wait(&bk->full[s], (j_qk / STAGES) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA);
-        if (!ok) return false;
+    // The whole warp takes every step and one elected thread issues: the descriptors then stay
+    // in uniform registers. (Inside a branch on lane == 0 an MMA cost 110 cycles to issue, with
+    // the elected thread about 60.)
+    const uint32_t elected = elect_one();
+    const uint32_t id_qk = idesc8<FMT>(2 * NQ, false), id_pv = idesc8<FMT>(2 * NQ, true);
+    const uint64_t k0 = tile_desc<D>(smem_u32(smem));
+    const uint64_t q0 = tile_desc<D>(smem_u32(smem) + SM::kQ);
+    const uint64_t p0 = tile_desc<SM::kPRow>(smem_u32(smem) + SM::kP);
+    // QK runs ahead of PV by as many tiles as there are buffers of S^T; whichever product has its
+    // operands goes next, so that neither a late tile holds up a finished P nor the other way.
+    int di = -1, left = 0;                 // descriptor, tiles left in it
+    int j_qk = 0, j_pv = 0;                // next tile of either product
+    bool ended = false, fresh = false;     // no more tiles; the run's queries are still to come
+    auto test = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    unsigned long long idle = 0;           // since when neither could go on
+    while (!ended || j_pv < j_qk) {
+      bool did = false;
+      if (!ended && left == 0 && test(&bk->d_full[(di + 1) % kDescs], ((di + 1) / kDescs) & 1)) {
+        if (di >= 0 && lane == 0) mbar_arrive(&bk->d_empty[di % kDescs]);
+        ++di;
+        left = bk->desc[di % kDescs].n;
+        __syncwarp();
+        ended = left == 0;
+        fresh = true;
+        did = true;
+      }
+      const int s = j_qk % STAGES;
+      if (left > 0 && j_qk - j_pv < SM::kS && (!fresh || test(&bk->q_full[di & 1], (di >> 1) & 1)) &&
+          test(&bk->full[s], (j_qk / STAGES) & 1)) {
         tc_fence_after();
+        const int qb = di & 1, sb = j_qk % SM::kS;
         const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
         const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
-#pragma unroll
-        for (int part = 0; part < (FMT == FOCUS_CACHE_E4M3 ? 2 : 1); ++part)
+        fresh = false;
+        --left;
+        if (elected) {
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks)
-            mma8<FMT>(tS + buf * SM::kAcc, kd + ks * 2, qd + part * (NQ * D / 16) + ks * 2, id_qk, part + ks > 0 ? 1u : 0u);
-        mma_commit(&bk->s_full[buf]);
-        if (--left == 0) mma_commit(&bk->q_empty[qb]);
+            mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id_qk, ks > 0 ? 1u : 0u);
+          mma_commit(&bk->s_full[sb]);
+          if (left == 0) mma_commit(&bk->q_empty[qb]);
+        }
+        __syncwarp();
         ++j_qk;
-        return true;
-      };
-      more = issue_qk();
-      for (int j = 0; ok && j < j_qk; ++j) {
-        if (more) more = issue_qk();
-        if (!ok) break;
-        const int buf = j & 1, s = j % STAGES;
-        ok = mbar_wait(&bk->p_full[buf], (j >> 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA);
-        if (!ok) break;
+        did = true;
+      }
+      const int buf = j_pv & 1;
+      if (j_pv < j_qk && test(&bk->p_full[buf], (j_pv >> 1) & 1)) {
         tc_fence_after();
-        const uint64_t vd = k0 + static_cast<uint64_t>((s * 2 + 1) * SM::kTile / 16);
+        const int sv = j_pv % STAGES;
+        const uint64_t vd = k0 + static_cast<uint64_t>((sv * 2 + 1) * SM::kTile / 16);
         const uint64_t pd = p0 + static_cast<uint64_t>(buf * SM::kPBuf / 16);
-#pragma unroll
-        for (int part = 0; part < (FMT == FOCUS_CACHE_E4M3 ? 2 : 1); ++part)
+        if (elected) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma8<FMT>(tO + buf * SM::kAcc, vd + ks * (32 * D / 16), pd + part * (NQ * 128 / 16) + ks * 2, id_pv,
-                      part + ks > 0 ? 1u : 0u);
-        mma_commit(&bk->o_full[buf]);
-        mma_commit(&bk->empty[s]);
+            mma8<FMT>(tO + buf * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id_pv, ks > 0 ? 1u : 0u);
+          mma_commit(&bk->o_full[buf]);
+          mma_commit(&bk->empty[sv]);
+        }
+        __syncwarp();
+        ++j_pv;
+        did = true;
       }
-      mma_commit(&bk->drain);
-      const unsigned long long w0 = globaltimer();
-      while (!mbar_try_wait(&bk->drain, 0) && globaltimer() - w0 < 500000000ull) {
+      if (did) {
+        idle = 0;
+      } else {
+        const unsigned long long now = globaltimer();
+        if (idle == 0) idle = now;
+        bool stop = *abort_flag != 0;
+        if (now - idle > kWaitLimitNs) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            record_dev_error(a.dev_err, DEV_ERR_TIMEOUT_MMA);
+          }
+          stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop)) break;
       }
+    }
+    if (elected) mma_commit(&bk->drain);
+    __syncwarp();
+    const unsigned long long w0 = globaltimer();
+    while (!mbar_try_wait(&bk->drain, 0) && globaltimer() - w0 < 500000000ull) {
     }
     __syncwarp();
   } else if (warp >= kQuery) {
     // ------------------------------------------------------------ query rows
-    // Query q of the slice (head kvh * g + r / qcap, row r % qcap of r = row0 + q) as hi and lo
-    // rows of the K-major B operand; two warps, a row to each in turn.
     bool ok = true;
     for (int di = 0; ok; ++di) {
       const int ds = di % kDescs, qb = di & 1;
@@ -728,81 +865,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1, abort_flag, a.dev_err,
                                                DEV_ERR_TIMEOUT_PRODUCER));
       if (!ok) break;
-      uint8_t* dst = smem + SM::kQ + qb * SM::kQBuf;
-      constexpr int E = D / 32;                  // elements of a lane
-      constexpr int UN = 4;                      // rows in flight
-      for (int q0 = warp - kQuery; q0 < NQ; q0 += 2 * UN) {
-        float x[UN][E];
-        int rows[UN];
-#pragma unroll
-        for (int i = 0; i < UN; ++i) {
-          const int q = q0 + 2 * i, r = d.row0 + q;
-          rows[i] = q;
-          const int qh = r / a.qcap, qi = r - qh * a.qcap;
-          const bool real = q < d.rows && qi < d.nq;
-          const __nv_bfloat16* src = a.Q + ((static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            uint32_t w = 0u;
-            if (real) w = __ldg(reinterpret_cast<const uint32_t*>(src) + e / 2);
-            x[i][e] = __uint_as_float(w << 16);
-            x[i][e + 1] = __uint_as_float(w & 0xffff0000u);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < UN; ++i) {
-          const int q = rows[i];
-          if (q >= NQ) continue;
-          float m = 0.f;
-          bool bad = false;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            m = fmaxf(m, fabsf(x[i][e]));
-            bad |= !(fabsf(x[i][e]) <= 3.4e38f);
-          }
-          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-          bad = __any_sync(0xffffffffu, bad);
-          float back;                            // what a unit of the row's codes stands for
-          uint32_t hi = 0, lo = 0;
-          if constexpr (FMT == FOCUS_CACHE_E4M3) {
-            // power of two that brings the largest element into [128, 256)
-            const int ex = m > 0.f ? max(-120, min(120, 7 - ilogbf(m))) : 0;
-            const float up = __int_as_float((127 + ex) << 23);
-            back = __int_as_float((127 - ex) << 23);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float y0 = (a.negative ? -x[i][e] : x[i][e]) * up, y1 = (a.negative ? -x[i][e + 1] : x[i][e + 1]) * up;
-              const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-              const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-              hi |= static_cast<uint32_t>(h) << (8 * e);
-              lo |= static_cast<uint32_t>(
-                        __nv_cvt_float2_to_fp8x2(make_float2(y0 - hf.x, y1 - hf.y), __NV_SATFINITE, __NV_E4M3))
-                    << (8 * e);
-            }
-          } else {
-            const float up = m > 1e-30f ? 16256.f / m : 0.f;
-            back = m > 1e-30f ? m / 16256.f : 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const int v = __float2int_rn((a.negative ? -x[i][e] : x[i][e]) * up), vh = (v + 64) >> 7;
-              hi |= static_cast<uint32_t>(vh & 0xff) << (8 * e);
-              lo |= static_cast<uint32_t>((v - (vh << 7)) & 0xff) << (8 * e);
-            }
-          }
-          const uint32_t at = row_chunk<D>(q, lane * E / 16) + (lane * E & 15);
-          if constexpr (E == 4) {
-            *reinterpret_cast<uint32_t*>(dst + at) = hi;
-            *reinterpret_cast<uint32_t*>(dst + NQ * D + at) = lo;
-          } else {
-            *reinterpret_cast<uint16_t*>(dst + at) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t*>(dst + NQ * D + at) = static_cast<uint16_t>(lo);
-          }
-          if (lane == 0) bk->q_scale[qb][q] = bad ? NAN : back * a.scale_log2;
-        }
-      }
+      // the first run's rows are shared with the softmax warps, which have nothing else to do yet
+      split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], warp - kQuery, di == 0 ? 10 : 2);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bk->q_full[qb]);
+      if (lane == 0) mbar_arrive_n(&bk->q_full[qb], di == 0 ? 1 : 5);
     }
   } else {
     // ------------------------------------------------------------ softmax groups
@@ -826,14 +893,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) d = bk->desc[ds];
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bk->d_empty[ds]);
+      if (ok && d.n > 0 && di == 0) {
+        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 2 + warp, 10);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bk->q_full[0]);
+      }
       if (ok && d.n > 0)
         ok = __all_sync(0xffffffffu, mbar_wait(&bk->q_full[qb], (di >> 1) & 1, abort_flag, a.dev_err,
                                                DEV_ERR_TIMEOUT_SOFTMAX));
       if (bar_red_or(bar, 128, !ok) || d.n == 0) break;      // the whole group leaves together
-      const float qs = bk->q_scale[qb][c0 + lc];
+      // (a zero query or scale: with the smallest normal number instead, every finite score is
+      // still 0, and a masked key's -infinity stays what it is)
+      const float qs_read = bk->q_scale[qb][c0 + lc];
+      const float qs = qs_read == 0.f ? 1.17549435e-38f : qs_read;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
-      float acc[NC], lsum[NC], m_run = -INFINITY;
+      // Sums over tiles are relative to 2^m_ref, which is the largest score of the run's first
+      // tile and moves up only when another tile's is 2^30 times as large: fp32 has the range, and
+      // no sum is rescaled tile by tile.
+      float acc[NC], lsum[NC], m_ref = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NC; ++n) acc[n] = lsum[n] = 0.f;
       // adds O^T of tile j, in its buffer, to the sums
@@ -844,24 +923,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  DEV_ERR_TIMEOUT_SOFTMAX));
         if (!ok) return;
         tc_fence_after();
-        uint32_t r[NC];
+        uint32_t r[NC], r2[NC];
         tmem_ld_cols<NC>(tO + buf * SM::kAcc + lane_addr + c0, r);
-        if constexpr (FMT == FOCUS_CACHE_INT8) {
-          uint32_t r2[NC];
-          tmem_ld_cols<NC>(tO + buf * SM::kAcc + NQ + lane_addr + c0, r2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int n = 0; n < NC; ++n)
-            r[n] = __float_as_uint(static_cast<float>(static_cast<int>(r[n]) * 128 + static_cast<int>(r2[n])));
-        } else {
-          tmem_ld_wait();
-        }
+        tmem_ld_cols<NC>(tO + buf * SM::kAcc + NQ + lane_addr + c0, r2);
+        tmem_ld_wait();
         const float4* f = reinterpret_cast<const float4*>(bk->post[warp][buf]);
 #pragma unroll
-        for (int n = 0; n < NC; n += 2) {
-          const float4 v = f[n / 2];
-          acc[n] = acc[n] * v.x + v.y * __uint_as_float(r[n]);
-          acc[n + 1] = acc[n + 1] * v.z + v.w * __uint_as_float(r[n + 1]);
+        for (int n = 0; n < NC; n += 4) {
+          const float4 v = f[n / 4];
+          acc[n] += v.x * both<FMT>(r[n], r2[n]);
+          acc[n + 1] += v.y * both<FMT>(r[n + 1], r2[n + 1]);
+          acc[n + 2] += v.z * both<FMT>(r[n + 2], r2[n + 2]);
+          acc[n + 3] += v.w * both<FMT>(r[n + 3], r2[n + 3]);
         }
         tc_fence_before();
       };
@@ -870,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j_first = kBoth ? jb : jb + ((jb ^ grp) & 1);
       bool left_early = false;
       for (int j = j_first; j < je; j += kStep) {
-        const int buf = j & 1, s = j % STAGES;
+        const int buf = j & 1, s = j % STAGES, sb = j % SM::kS;
         if (j - 2 >= jb) collect(j - 2);
         if (ok)
           ok = __all_sync(0xffffffffu, mbar_wait(&bk->full[s], (j / STAGES) & 1, abort_flag, a.dev_err,
@@ -883,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           masked = bk->masked[s] != 0;
           vmax = bk->vmax[s];
           if (masked) on = bk->valid[s][t] != 0;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bk->s_full[buf], (j >> 1) & 1, abort_flag, a.dev_err,
+          ok = __all_sync(0xffffffffu, mbar_wait(&bk->s_full[sb], (j / SM::kS) & 1, abort_flag, a.dev_err,
                                                  DEV_ERR_TIMEOUT_SOFTMAX));
         }
         float x[NC];
@@ -891,20 +964,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < NC; ++n) x[n] = 0.f;
         if (ok) {
           tc_fence_after();
-          uint32_t r[NC];
-          tmem_ld_cols<NC>(tS + buf * SM::kAcc + lane_addr + c0, r);
-          if constexpr (FMT == FOCUS_CACHE_INT8) {
-            uint32_t r2[NC];
-            tmem_ld_cols<NC>(tS + buf * SM::kAcc + NQ + lane_addr + c0, r2);
-            tmem_ld_wait();
+          uint32_t r[NC], r2[NC];
+          tmem_ld_cols<NC>(tS + sb * SM::kAcc + lane_addr + c0, r);
+          tmem_ld_cols<NC>(tS + sb * SM::kAcc + NQ + lane_addr + c0, r2);
+          tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-              x[n] = static_cast<float>(static_cast<int>(r[n]) * 128 + static_cast<int>(r2[n])) * key.x;
-          } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int n = 0; n < NC; ++n) x[n] = __uint_as_float(r[n]) * key.x;
-          }
+          for (int n = 0; n < NC; ++n) x[n] = both<FMT>(r[n], r2[n]) * key.x;
         }
         if (masked && !on) {
 #pragma unroll
@@ -912,12 +977,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the largest of each column: over the warp, then over the group's four warps; lane n of
         // every warp follows column n
-        float mine = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
           const float m = warp_max_nan(x[n]);
-          mine = lane == n ? m : mine;
+          top[n & 3] = lane == n ? m : top[n & 3];
         }
+        const float mine = (lane & 2) ? ((lane & 1) ? top[3] : top[2]) : ((lane & 1) ? top[1] : top[0]);
         par ^= 1;
         if (lane < NC) bk->red[grp][par][wq][lane] = mine;
         if (bar_red_or(bar, 128, !ok)) {
@@ -928,59 +994,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float* rd = &bk->red[grp][par][0][0];
           const float mt = max_nan(max_nan(rd[lc], rd[32 + lc]), max_nan(rd[64 + lc], rd[96 + lc]));
           const float ms = mt == -INFINITY ? -INFINITY : mt * qs;      // in units of log2
-          const float mn = max_nan(m_run, ms);
-          // reference of this tile's probabilities: e4m3 the running maximum (its range has room
-          // below), int8 the tile's own, whose fixed point is then never wasted
-          const float ref = FMT == FOCUS_CACHE_E4M3 ? mn : ms;
-          const float al = m_run == -INFINITY ? 0.f : exp2_approx(m_run - mn);
-          const float be = FMT == FOCUS_CACHE_E4M3 ? 1.f : ms == -INFINITY ? 0.f : exp2_approx(ms - mn);
-          m_run = mn;
+          // The tile's probabilities are relative to its own largest score. Against the running
+          // maximum instead, all that lies 2^-18 below one large key (an attention sink) would be
+          // rounded away, and with thousands of such keys a part of the result; so, no more than
+          // 128 * 2^-18 of a tile's own largest is.
+          float al = 1.f;
+          if (ms > m_ref + 30.f || (m_ref == -INFINITY && ms > -INFINITY)) {
+            al = exp2_approx(m_ref - ms);
+            m_ref = ms;
+          }
+          const float be = ms == -INFINITY ? 0.f : exp2_approx(ms - m_ref);
           __syncwarp();                                                // the last tile's factors have been read
+          if (__any_sync(0xffffffffu, al != 1.f)) {                    // the same in the group's four warps
+            if (lane < NC) {
+              bk->be[warp][lane] = al;
+              bk->post[warp][buf ^ 1][lane] *= al;                     // a product that is still under way
+            }
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              const float f = bk->be[warp][n];
+              lsum[n] *= f;
+              acc[n] *= f;
+            }
+            __syncwarp();
+          }
           if (lane < NC) {
-            bk->pre[warp][lane] = make_float2(qs, ref == -INFINITY ? 0.f : -ref);
-            bk->al[warp][lane] = al;
-            if (FMT == FOCUS_CACHE_INT8) bk->be[warp][lane] = be;
-            bk->post[warp][buf][lane] = make_float2(al, be * vmax);
+            bk->pre[warp][lane] = make_float2(qs, ms == -INFINITY ? 0.f : -ms);
+            bk->be[warp][lane] = be;
+            bk->post[warp][buf][lane] = be * vmax;
           }
           __syncwarp();
         }
         const float4* pre = reinterpret_cast<const float4*>(bk->pre[warp]);
-        const float4* pal = reinterpret_cast<const float4*>(bk->al[warp]);
         const float4* pbe = reinterpret_cast<const float4*>(bk->be[warp]);
-        uint8_t* prow = smem + SM::kP + buf * SM::kPBuf + (t & 15);
+        // P is written as it is held, a key to a row, hi then lo: an MN-major operand. (Stored
+        // query-major, a byte at a time, the stores alone took 1500 cycles of a tile.)
+        uint8_t* pbuf = smem + SM::kP + buf * SM::kPBuf;
 #pragma unroll
-        for (int n = 0; n < NC; n += 4) {
-          const float4 e0 = pre[n / 2], e1 = pre[n / 2 + 1], al = pal[n / 4];
-          float p[4];
-          p[0] = exp2_approx(x[n] * e0.x + e0.y);
-          p[1] = exp2_approx(x[n + 1] * e0.z + e0.w);
-          p[2] = exp2_approx(x[n + 2] * e1.x + e1.y);
-          p[3] = exp2_approx(x[n + 3] * e1.z + e1.w);
-          if (masked && !on) p[0] = p[1] = p[2] = p[3] = 0.f;
-          if constexpr (FMT == FOCUS_CACHE_INT8) {
-            const float4 be = pbe[n / 4];
-            lsum[n] = lsum[n] * al.x + p[0] * be.x;
-            lsum[n + 1] = lsum[n + 1] * al.y + p[1] * be.y;
-            lsum[n + 2] = lsum[n + 2] * al.z + p[2] * be.z;
-            lsum[n + 3] = lsum[n + 3] * al.w + p[3] * be.w;
-          } else {
-            lsum[n] = lsum[n] * al.x + p[0];
-            lsum[n + 1] = lsum[n + 1] * al.y + p[1];
-            lsum[n + 2] = lsum[n + 2] * al.z + p[2];
-            lsum[n + 3] = lsum[n + 3] * al.w + p[3];
-          }
-          uint32_t hi, lo;
+        for (int n0 = 0; n0 < NC; n0 += 16) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            split2<FMT>(p[e] * key.y, p[e + 1] * key.y, hi, lo);
-            const int q = c0 + n + e;
-            const uint32_t o0 = q * 128 + (((t >> 4) ^ (q & 7)) << 4);
-            const uint32_t o1 = (q + 1) * 128 + (((t >> 4) ^ ((q + 1) & 7)) << 4);
-            prow[o0] = static_cast<uint8_t>(hi);
-            prow[o1] = static_cast<uint8_t>(hi >> 8);
-            prow[NQ * 128 + o0] = static_cast<uint8_t>(lo);
-            prow[NQ * 128 + o1] = static_cast<uint8_t>(lo >> 8);
+          for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 4 * i;
+            const float4 e0 = pre[n / 2], e1 = pre[n / 2 + 1], be = pbe[n / 4];
+            float p[4];
+            p[0] = exp2_approx(x[n] * e0.x + e0.y);
+            p[1] = exp2_approx(x[n + 1] * e0.z + e0.w);
+            p[2] = exp2_approx(x[n + 2] * e1.x + e1.y);
+            p[3] = exp2_approx(x[n + 3] * e1.z + e1.w);
+            lsum[n] += p[0] * be.x;
+            lsum[n + 1] += p[1] * be.y;
+            lsum[n + 2] += p[2] * be.z;
+            lsum[n + 3] += p[3] * be.w;
+            split4<FMT>(p, key.y, hi[i], lo[i]);
           }
+          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (c0 + n0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (NQ + c0 + n0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         // A masked key's values may be anything, NaN codes included, and 0 * NaN is NaN
         if (FMT == FOCUS_CACHE_E4M3 && masked && !on && (!kBoth || grp == 0)) {
@@ -1036,16 +1106,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float v = grp == 0 ? acc[HC + i] : acc[i];
           xch[(grp * HC + i) * 128 + t] = v;
         }
-        if (wq == 0 && lane < NC) bk->xml[grp][lane] = make_float2(m_run, l);
+        if (wq == 0 && lane < NC) bk->xml[grp][lane] = make_float2(m_ref, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bk->x_full);
         ok = __all_sync(0xffffffffu, mbar_wait(&bk->x_full, (2 * n_x + 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_EPILOGUE));
         if (bar_red_or(bar, 128, !ok)) break;
         const float2 om = bk->xml[1 - grp][lc];
-        const float M = max_nan(m_run, om.x);
-        const float ca = l == 0.f ? 0.f : exp2_approx(m_run - M), cb = om.y == 0.f ? 0.f : exp2_approx(om.x - M);
+        const float M = max_nan(m_ref, om.x);
+        const float ca = l == 0.f ? 0.f : exp2_approx(m_ref - M), cb = om.y == 0.f ? 0.f : exp2_approx(om.x - M);
         l = ca * l + cb * om.y;
-        m_run = M;
+        m_ref = M;
         n0 = grp * HC;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
@@ -1075,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (d.slot >= 0 && wq == 0 && lane >= n0 && lane < n0 + OC && c0 + lane < d.rows)
-        a.part_ml[static_cast<size_t>(d.slot) * NQ + c0 + lane] = make_float2(m_run, l);
+        a.part_ml[static_cast<size_t>(d.slot) * NQ + c0 + lane] = make_float2(m_ref, l);
     }
     if (!ok) bk->abort_flag = 1;
   }
