@@ -29,10 +29,13 @@
 // writes zeros for the units without keys. So one long sequence among short ones still fills
 // the GPU, and a sequence's length is only read on the device.
 //
-// Warps: 0-3 and 4-7 two softmax groups, 8 producer (TMA for pages, cp.async for sink rows),
-// 9 tcgen05.mma issuer and TMEM owner, 10-11 query rows. Up to 32 query rows the two groups
-// take tiles in turn, each with its own running maximum, and join at the end of a unit; with
-// 64 rows both work on every tile, 32 columns each.
+// Warps: 0-3 and 4-7 two softmax groups, 8 and 9 producers, a tile each in turn (TMA for pages,
+// cp.async for sink rows), 10 and 11 issue the products S^T and O^T (10 owns tensor memory and
+// prepares the query rows). A softmax thread owns a key and up to 32 query columns. Up to 32 query
+// rows the two groups take tiles in turn and join their sums at the end of a unit; with 64 rows
+// both work on every tile, 32 columns each. Twelve warps leave 168 registers to a thread: with four
+// groups of 16 columns (20 warps, 96 registers) the sums spilled, and a spilled register costs
+// 500 cycles beside a shared memory that leaves no L1.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,10 +47,15 @@
 namespace focus {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kProducer = 8, kMma = 9, kQuery = 10;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kProducers = 2;
+constexpr int kProducer = kSoftmaxWarps, kMmaS = kProducer + kProducers, kMmaO = kMmaS + 1;
+constexpr int kThreads = (kMmaO + 1) * 32;
+constexpr int kQParts = kSoftmaxWarps + 1;   // warps that prepare the first queries
 constexpr int kMaxList = 1024;          // sinks, kept blocks
 constexpr int kDescs = 4;
+constexpr int kMasked = 1, kByKey = 2;
+constexpr int kLead = 2;                // places of a unit before its first tile (see unit_length)
 
 struct CacheAttnArgs {
   const __nv_bfloat16* Q;
@@ -63,7 +71,7 @@ struct CacheAttnArgs {
   __nv_bfloat16* O;
   float* part_o;             // [2 grid][NQ][d]
   float2* part_ml;           // [2 grid][NQ]
-  int table_cols, n_pages, page, B, Hq, Hkv, g, qcap, G, S, C;
+  int table_cols, n_pages, page, page_shift, B, Hq, Hkv, g, qcap, G, S, C;
   int n_slices, slice_rows;  // the g * qcap query rows of a KV head in slices
   int grid;
   float scale_log2;          // |scale| log2(e); the sign goes into the queries
@@ -89,12 +97,12 @@ __device__ __forceinline__ Sequence sequence_of(const CacheAttnArgs& a, int b) {
     s.gs = max(0, min(g0, top));
     s.ge = static_cast<int>(max(0LL, min(static_cast<long long>(g0) + a.G, static_cast<long long>(top))));
     s.P = max(0, min(a.P[b], s.gs));
-    s.n_gen = s.ge > s.gs ? (s.ge - 1) / a.page - s.gs / a.page + 1 : 0;
+    s.n_gen = s.ge > s.gs ? ((s.ge - 1) >> a.page_shift) - (s.gs >> a.page_shift) + 1 : 0;
     s.n_pages = s.n_gen + a.C;
     s.tiles = (s.n_pages * a.page + a.S + 127) >> 7;
   } else {
     s.len = max(0, min(a.lens[b], top));
-    s.n_pages = (s.len + a.page - 1) / a.page;
+    s.n_pages = (s.len + a.page - 1) >> a.page_shift;
     s.tiles = (s.len + 127) >> 7;
   }
   return s;
@@ -102,27 +110,32 @@ __device__ __forceinline__ Sequence sequence_of(const CacheAttnArgs& a, int b) {
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// Tiles of the units of one head slice of all sequences (a warp; the same in every lane).
+// Tiles lie on an axis on which every unit also takes kLead places before its first tile, for
+// what a run costs beyond its tiles (query rows, joining the groups, output): shares of equal
+// length then take about as long, whether they hold one long unit or many short ones.
+__device__ __forceinline__ int unit_length(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
+
+// Length of the axis for one head slice of all sequences (a warp; the same in every lane).
 template <bool SPARSE>
-__device__ __forceinline__ int tiles_of_all(const CacheAttnArgs& a) {
+__device__ __forceinline__ int length_of_all(const CacheAttnArgs& a) {
   int n = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) n += warp_sum(b0 + lane_id() < a.B ? sequence_of<SPARSE>(a, b0 + lane_id()).tiles : 0);
+  for (int b0 = 0; b0 < a.B; b0 += 32) n += warp_sum(b0 + lane_id() < a.B ? unit_length(sequence_of<SPARSE>(a, b0 + lane_id()).tiles) : 0);
   return n;
 }
 
-// Tiles of sequences before b.
+// The part of it before sequence b.
 template <bool SPARSE>
-__device__ __forceinline__ int tiles_before(const CacheAttnArgs& a, int b) {
+__device__ __forceinline__ int length_before(const CacheAttnArgs& a, int b) {
   int n = 0;
-  for (int b0 = 0; b0 < b; b0 += 32) n += warp_sum(b0 + lane_id() < b ? sequence_of<SPARSE>(a, b0 + lane_id()).tiles : 0);
+  for (int b0 = 0; b0 < b; b0 += 32) n += warp_sum(b0 + lane_id() < b ? unit_length(sequence_of<SPARSE>(a, b0 + lane_id()).tiles) : 0);
   return n;
 }
 
-// Share i of `shares` contiguous shares of T tiles begins at tile i * T / shares.
+// Share i of `shares` contiguous shares of an axis of length T begins at i * T / shares.
 __device__ __forceinline__ int share_begin(int i, int T, int shares) {
   return static_cast<int>(static_cast<long long>(i) * T / shares);
 }
-// The share that tile x falls in.
+// The share that place x falls in.
 __device__ __forceinline__ int share_of(int x, int T, int shares) {
   return static_cast<int>((static_cast<long long>(x + 1) * shares - 1) / T);
 }
@@ -135,48 +148,65 @@ struct Desc {               // a run of tiles of one unit that this CTA works on
   int slot;                 // where the partial result goes, -1 = straight into O
 };
 
-template <int NQ, int STAGES>
+// How a tile's NQ query columns are spread over the groups, and what is buffered.
+template <int NQ>
+struct Split {
+  static constexpr int kC = NQ < 32 ? NQ : 32;         // query columns of a softmax thread
+  static constexpr int kPer = NQ / kC;                 // groups of a tile
+  static constexpr int kSlots = 2 / kPer;              // tiles worked on in turn
+  static constexpr int kBuf = kSlots;                  // buffers of P and O^T
+  static constexpr int kS = 2 * kBuf;                  // buffers of S^T
+  static constexpr int kStages = NQ == 64 ? 4 : 5;
+};
+
+template <int NQ>
 struct __align__(16) Book {
-  uint64_t full[STAGES], empty[STAGES];
-  uint64_t s_full[4], p_full[2], o_full[2];
+  using Sp = Split<NQ>;
+  static constexpr int NC = Sp::kC;
+  uint64_t full[Sp::kStages], empty[Sp::kStages];
+  uint64_t s_full[Sp::kS], s_free[Sp::kS], p_full[Sp::kBuf], o_full[Sp::kBuf];
   uint64_t q_full[2], q_empty[2];
   uint64_t d_full[kDescs], d_empty[kDescs];
-  uint64_t x_full, x_done, drain;
+  uint64_t x_full, x_done, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   Desc desc[kDescs];
   // (arrays that are read four floats at a time start on 16 bytes)
-  alignas(16) float2 key[STAGES][128];  // (scale of the key, factor of the value relative to the tile's largest)
-  alignas(16) uint8_t valid[STAGES][128];
-  float vmax[STAGES];                   // largest scale of a value in the tile
-  int masked[STAGES];                   // some key of the tile is masked
-  float q_scale[2][NQ];
-  float red[2][2][4][32];               // [group][parity][warp][column]
-  alignas(16) float2 pre[8][32];        // [warp][column]: (query scale, -reference)
-  alignas(16) float be[8][32];          // [warp][column]: factor of the tile's row sum
-  alignas(16) float post[8][2][32];     // [warp][buffer][column]: factor of the tile's O
-  alignas(16) float2 xml[2][32];        // (m, l) of the other group's columns
-  int blk[kMaxList], snk[kMaxList];
+  // scales of a tile: a page's (key scale, value scale relative to the tile's largest, first and
+  // last row that are keys), or with sinks among them each key's
+  alignas(16) float4 page[Sp::kStages][8];
+  alignas(16) float2 key[Sp::kStages][128];
+  alignas(16) uint8_t valid[Sp::kStages][128];
+  float vmax[Sp::kStages];              // largest scale of a value in the tile
+  int info[Sp::kStages];                // kMasked: some key is masked, kByKey: scales key by key
+  alignas(16) float q_scale[2][NQ];
+  alignas(16) float red[2][2][4][NC];   // [group][parity][warp][column]
+  alignas(16) float qs[kSoftmaxWarps][NC];       // [warp][column]: scale of the query
+  alignas(16) uint16_t ref[kSoftmaxWarps][NC];   // [warp][column], bf16: -reference of the tile's probabilities
+  alignas(16) uint16_t be[kSoftmaxWarps][NC];    // [warp][column], bf16: factor from it to the run's reference
+  alignas(16) float2 xml[2][NC];        // (m, l) of a group's columns
+  int blk[kProducers][kMaxList], snk[kProducers][kMaxList];   // a producer's lists of its unit
 };
 
 template <int FMT, int D, int NQ>
 struct Lay {
-  static constexpr int kStages = NQ == 64 ? 4 : 5;
+  using Sp = Split<NQ>;
   static constexpr uint32_t kTile = 128 * D;                       // bytes of a K or V tile
-  static constexpr uint32_t kQ = kStages * 2 * kTile;              // 2 buffers of hi, lo rows
+  static constexpr uint32_t kQ = Sp::kStages * 2 * kTile;          // 2 buffers of hi, lo rows
   static constexpr uint32_t kQBuf = 2 * NQ * D;
   static constexpr uint32_t kP = kQ + 2 * kQBuf;
   static constexpr uint32_t kPRow = 2 * NQ;                        // bytes of a key's row of P: hi, lo
   static constexpr uint32_t kPBuf = 128 * kPRow;
-  static constexpr uint32_t kBook = kP + 2 * kPBuf;
-  static constexpr uint32_t kBytes = kBook + sizeof(Book<NQ, kStages>) + 1024;
+  // the groups of the same columns hand each other what the others put out, through the P buffers
+  static constexpr uint32_t kX = 2 * (Sp::kC - Sp::kC / Sp::kSlots) * 128 * 4;
+  static constexpr uint32_t kBook = kP + (Sp::kBuf * kPBuf > kX ? Sp::kBuf * kPBuf : kX);
+  using Bk = Book<NQ>;
+  static constexpr uint32_t kBytes = kBook + sizeof(Bk) + 1024;
   static constexpr int kAcc = 2 * NQ;                              // accumulator columns of a product: hi, lo
-  static constexpr int kS = NQ == 64 ? 2 : 4;                      // buffers of S^T
-  static constexpr uint32_t kTmemUsed = (kS + 2) * kAcc;
+  static constexpr uint32_t kTmemUsed = (Sp::kS + Sp::kBuf) * kAcc;
   static constexpr uint32_t kTmem = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
   static_assert(kTmemUsed <= 512, "exceeds tensor memory");
-  using Bk = Book<NQ, kStages>;
   static_assert(kBook % 16 == 0 && alignof(Bk) == 16, "shared-memory alignment");
 };
 
@@ -231,10 +261,21 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t 
   }
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // Largest of a float over the warp, NaN if any is NaN.
 __device__ __forceinline__ float warp_max_nan(float v) {
   float r;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -252,6 +293,37 @@ __device__ __forceinline__ uint32_t elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(e));
   return e;
+}
+
+// Waits for phase `parity` (a whole warp). The thread sleeps in the barrier for as long as the
+// hint says (a wait that polls takes issue slots from the warps that have work); false when the
+// limit runs out or another warp gave up.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* dev_err, int code) {
+  const unsigned long long t0 = globaltimer();
+  while (!__all_sync(0xffffffffu, mbar_sleep(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
+      *abort_flag = 1;
+      if (lane_id() == 0) record_dev_error(dev_err, code);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* dev_err, int code) {
+  if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
+  return wait_slow(bar, parity, abort_flag, dev_err, code);
 }
 
 // n arrivals at once.
@@ -272,35 +344,58 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// hi and lo of four probabilities p times f (256 for e4m3, 16256 for int8, times the value's
-// relative scale), a byte each, column 0 lowest.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+// hi and lo of four probabilities (in units of 1/256 for e4m3, 1/16256 for int8), a byte each,
+// column 0 lowest.
 template <int FMT>
-__device__ __forceinline__ void split4(const float (&p)[4], float f, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split4(float2 p01, float2 p23, uint32_t& hi, uint32_t& lo) {
   if constexpr (FMT == FOCUS_CACHE_E4M3) {
-    uint32_t h[2], l[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // in half precision: 11 bits hold p to 2^-12, and p - hi is exact
-      const __half2 x = __floats2half2_rn(p[2 * i] * f, p[2 * i + 1] * f);
-      h[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-      const __half2 r = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3)));
-      l[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
-    }
-    hi = __byte_perm(h[0], h[1], 0x5410);
-    lo = __byte_perm(l[0], l[1], 0x5410);
+    // the rest in half precision: 11 bits hold p to 2^-12, and p - hi is exact
+    const __half2 x0 = __floats2half2_rn(p01.x, p01.y), x1 = __floats2half2_rn(p23.x, p23.y);
+    const __nv_fp8x2_storage_t h0 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x0), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t h1 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x1), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r0 = __hsub2(x0, __half2(__nv_cvt_fp8x2_to_halfraw2(h0, __NV_E4M3)));
+    const __half2 r1 = __hsub2(x1, __half2(__nv_cvt_fp8x2_to_halfraw2(h1, __NV_E4M3)));
+    const __nv_fp8x2_storage_t l0 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r0), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t l1 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r1), __NV_SATFINITE, __NV_E4M3);
+    // (packed by byte_perm: packed by mov.b32 {h0, h1}, ptxas 12.9 read h0 back from the wrong half)
+    hi = __byte_perm(h0, h1, 0x5410);
+    lo = __byte_perm(l0, l1, 0x5410);
   } else {
-    // v = round(p f) + 64 by adding 1.5 * 2^23 + 64: v = 128 hi + (lo + 64) with lo + 64 in
+    // v = round(p) + 64 by adding 1.5 * 2^23 + 64: v = 128 hi + (lo + 64) with lo + 64 in
     // [0, 128), in the low 15 bits of the sum
-    uint32_t h[2], l[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t a = __float_as_uint(fmaf(p[2 * i], f, 12582976.f)), b = __float_as_uint(fmaf(p[2 * i + 1], f, 12582976.f));
-      const uint32_t w = __byte_perm(a, b, 0x5410);
-      h[i] = (w >> 7) & 0x00ff00ffu;
-      l[i] = (w & 0x007f007fu) + 0x00c000c0u;      // lo mod 256 in bits 0-7 and 16-23
-    }
-    hi = __byte_perm(h[0], h[1], 0x6420);
-    lo = __byte_perm(l[0], l[1], 0x6420);
+    const float2 c = make_float2(12582976.f, 12582976.f);
+    const float2 a = add2(p01, c), b = add2(p23, c);
+    const uint32_t w0 = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x5410);
+    const uint32_t w1 = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x5410);
+    hi = __byte_perm((w0 >> 7) & 0x00ff00ffu, (w1 >> 7) & 0x00ff00ffu, 0x6420);
+    // lo mod 256 in bits 0-7 and 16-23
+    lo = __byte_perm((w0 & 0x007f007fu) + 0x00c000c0u, (w1 & 0x007f007fu) + 0x00c000c0u, 0x6420);
   }
 }
 
@@ -311,6 +406,18 @@ __device__ __forceinline__ float both(uint32_t hi, uint32_t lo) {
   else return static_cast<float>(static_cast<int>(hi) * 128 + static_cast<int>(lo));
 }
 
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int FMT>
+__device__ __forceinline__ float2 both2(const uint32_t* hi, const uint32_t* lo) {
+  if constexpr (FMT == FOCUS_CACHE_E4M3)
+    return add2(make_float2(__uint_as_float(hi[0]), __uint_as_float(hi[1])),
+                make_float2(__uint_as_float(lo[0]), __uint_as_float(lo[1])));
+  else
+    return make_float2(both<FMT>(hi[0], lo[0]), both<FMT>(hi[1], lo[1]));
+}
+
 template <int FMT>
 constexpr float prob_top() {
   return FMT == FOCUS_CACHE_E4M3 ? 256.f : 16256.f;
@@ -319,10 +426,10 @@ constexpr float prob_top() {
 // Query q of the slice (head kvh * g + r / qcap, row r % qcap of r = row0 + q) as hi and lo rows
 // of the K-major B operand: a warp, rows first, first + step, ...
 template <int FMT, int D, int NQ>
-__device__ __noinline__ void split_queries(const CacheAttnArgs& a, const Desc& d, uint8_t* dst, float* q_scale, int first,
+__device__ __forceinline__ void split_queries(const CacheAttnArgs& a, const Desc& d, uint8_t* dst, float* q_scale, int first,
                                            int step) {
   constexpr int E = D / 32;                  // elements of a lane
-  constexpr int UN = 4;                      // rows in flight
+  constexpr int UN = 8;                      // rows in flight
   const int lane = lane_id();
   for (int q0 = first; q0 < NQ; q0 += step * UN) {
     float x[UN][E];
@@ -399,12 +506,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
   using SM = Lay<FMT, D, NQ>;
-  constexpr int STAGES = SM::kStages;
-  constexpr bool kBoth = NQ == 64;               // both groups work on every tile
-  constexpr int NC = kBoth ? 32 : NQ;            // columns of a softmax thread
+  using Sp = Split<NQ>;
+  constexpr int STAGES = Sp::kStages;
+  constexpr int NC = Sp::kC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  auto* bk = reinterpret_cast<Book<NQ, STAGES>*>(smem + SM::kBook);
+  auto* bk = reinterpret_cast<Book<NQ>*>(smem + SM::kBook);
   volatile int* abort_flag = &bk->abort_flag;
   const int warp = warp_id(), lane = lane_id();
 
@@ -413,26 +520,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk->full[i], 2);                // the copies' bytes, the keys' scales
       mbar_init(&bk->empty[i], 1);
     }
-    for (int i = 0; i < SM::kS; ++i) mbar_init(&bk->s_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bk->p_full[i], kBoth ? 8 : 4);
+    for (int i = 0; i < Sp::kS; ++i) {
+      mbar_init(&bk->s_full[i], 2);              // the product, and the warp that has seen the tile's scales
+      mbar_init(&bk->s_free[i], 4 * Sp::kPer);
+    }
+    for (int i = 0; i < Sp::kBuf; ++i) {
+      mbar_init(&bk->p_full[i], 4 * Sp::kPer);
       mbar_init(&bk->o_full[i], 1);
-      mbar_init(&bk->q_full[i], 10);             // the query and the softmax warps
-      mbar_init(&bk->q_empty[i], 9);             // the last QK, and the softmax warps that read the scales
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bk->q_full[i], kQParts);
+      mbar_init(&bk->q_empty[i], 1 + kSoftmaxWarps);   // the last QK, and the warps that read the scales
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&bk->d_full[i], 1);
-      mbar_init(&bk->d_empty[i], 11);            // softmax, query and MMA warps
+      mbar_init(&bk->d_empty[i], kSoftmaxWarps + 2);   // softmax and MMA warps
     }
-    mbar_init(&bk->x_full, 8);
-    mbar_init(&bk->x_done, 8);
-    mbar_init(&bk->drain, 1);
+    mbar_init(&bk->x_full, kSoftmaxWarps);
+    mbar_init(&bk->x_done, kSoftmaxWarps);
+    mbar_init(&bk->drain[0], 1);
+    mbar_init(&bk->drain[1], 1);
     bk->abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == kMma) {
+  if (warp == kMmaS) {
     tmem_alloc(&bk->tmem_base, SM::kTmem);
     tmem_relinquish();
   }
@@ -442,22 +555,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t tmem = bk->tmem_base;
-  const uint32_t tS = tmem, tO = tmem + SM::kS * SM::kAcc;
+  const uint32_t tS = tmem, tO = tmem + Sp::kS * SM::kAcc;
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------ producer
-    const int all = tiles_of_all<SPARSE>(a);
+  if (warp >= kProducer && warp < kProducer + kProducers) {
+    // ------------------------------------------------------------ producers
+    // Both walk over all runs; tile j of the CTA is producer j % 2's. (One alone, with about 1800
+    // cycles a tile for the copies' issue, the scales and the wait, was slower than the memory.)
+    const int pw = warp - kProducer;
+    int* const blk_s = bk->blk[pw];
+    int* const snk_s = bk->snk[pw];
+    const int all = length_of_all<SPARSE>(a);
     const int heads = a.Hkv * a.n_slices;
     const int T = all * heads;
     const int shares = min(static_cast<int>(gridDim.x), T);
-    int issued = 0;                              // tiles whose copies are under way or done
+    int n_tiles = 0;                             // tiles of the runs so far
+    int issued = 0;                              // tiles up to here have their copies under way (this producer's)
     bool ok = true;
     int n_desc = 0;
-    auto push = [&](const Desc& d) {             // lane 0 publishes a run
+    auto push = [&](const Desc& d) {             // the first producer publishes a run
+      if (pw != 0) return;
       const int s = n_desc % kDescs;
       if (n_desc >= kDescs)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->d_empty[s], ((n_desc / kDescs) - 1) & 1, abort_flag, a.dev_err,
-                                               DEV_ERR_TIMEOUT_PRODUCER));
+        ok = wait_phase(&bk->d_empty[s], ((n_desc / kDescs) - 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_PRODUCER);
       if (!ok) return;
       if (lane == 0) {
         bk->desc[s] = d;
@@ -468,10 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (static_cast<int>(blockIdx.x) < shares) {
       const int t0 = share_begin(blockIdx.x, T, shares), t1 = share_begin(blockIdx.x + 1, T, shares);
-      // the sequence that tile t0 falls in
-      int b = 0, base = 0;                       // base: tiles of the sequences before b, all heads
+      // the sequence that place t0 falls in
+      int b = 0, base = 0;                       // base: length of the sequences before b, all heads
       for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int n = b0 + lane < a.B ? sequence_of<SPARSE>(a, b0 + lane).tiles * heads : 0;
+        const int n = b0 + lane < a.B ? unit_length(sequence_of<SPARSE>(a, b0 + lane).tiles) * heads : 0;
         int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -490,23 +609,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       Sequence q = sequence_of<SPARSE>(a, b);
       const uint64_t policy = l2_evict_first_policy();
       const bool once = a.n_slices == 1;         // the codes are read by this unit alone
-      const int ppt = 128 / a.page;              // pages of a tile
+      const int tp = 7 - a.page_shift;           // a tile is 2^tp pages
+      const int ppt = 1 << tp;
       const int32_t* trow = a.table + static_cast<size_t>(b) * a.table_cols;
       bool lists_sorted = true;
       int n_snk = 0;
       for (int t = t0; t < t1 && ok;) {
-        while (q.tiles * heads <= t - base) {    // on to the next sequence that has tiles
-          base += q.tiles * heads;
+        while (unit_length(q.tiles) * heads <= t - base) {    // on to the next sequence that has tiles
+          base += unit_length(q.tiles) * heads;
           ++b;
           q = sequence_of<SPARSE>(a, b);
           trow = a.table + static_cast<size_t>(b) * a.table_cols;
         }
-        const int u = (t - base) / q.tiles;      // KV head and slice
-        const int first = t - base - u * q.tiles, last = min(q.tiles, first + t1 - t);
+        const int len = unit_length(q.tiles), u = (t - base) / len;      // KV head and slice
+        const int at = base + u * len + kLead;                           // place of the unit's first tile
+        const int first = max(0, t - at), last = min(q.tiles, t1 - at);
+        t = at + q.tiles;
+        if (last <= first) continue;
         const int kvh = u / a.n_slices, slice = u - kvh * a.n_slices;
         Desc d;
         d.n = last - first;
-        d.j0 = issued;
+        d.j0 = n_tiles;
         d.b = b;
         d.kvh = kvh;
         d.row0 = slice * a.slice_rows;
@@ -515,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         d.slot = d.n == q.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (first == 0 ? 1 : 0);
         push(d);
         if (!ok) break;
-        t += d.n;
 
         if (SPARSE) {
           // the kept blocks: repeated entries are dropped (in an ascending list they are neighbours)
@@ -528,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int prev = __shfl_up_sync(0xffffffffu, v, 1);
             const int pv = lane == 0 ? before : prev;
             up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i > 0);
-            if (i < a.C) bk->blk[i] = v;
+            if (i < a.C) blk_s[i] = v;
             before = __shfl_sync(0xffffffffu, v, 31);
           }
           lists_sorted = __all_sync(0xffffffffu, up);
@@ -539,9 +661,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int i = i0 + lane;
               bool again = false;
               if (i < a.C)
-                for (int j = 0; j < i && !again; ++j) again = bk->blk[j] == bk->blk[i];
+                for (int j = 0; j < i && !again; ++j) again = blk_s[j] == blk_s[i];
               __syncwarp();
-              if (again) bk->blk[i] = -1;
+              if (again) blk_s[i] = -1;
               __syncwarp();
             }
           }
@@ -553,9 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         struct Batch {
           int raw, lo, hi, pg;
           float ks, vs;
+          float f, vm;                           // value scale relative to the tile's largest, that
+          unsigned part;                         // lanes whose page is not all keys
         };
         auto look_up = [&](int slot) {
-          Batch x{-1, 0, 0, -1, 0.f, 0.f};
+          Batch x{-1, 0, 0, -1, 0.f, 0.f, 0.f, 0.f, 0u};
           int col = -1;
           if (!SPARSE) {
             if (slot < q.n_pages) {
@@ -563,11 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               x.hi = min(a.page, q.len - slot * a.page);
             }
           } else if (slot < q.n_gen) {
-            col = q.gs / a.page + slot;
+            col = (q.gs >> a.page_shift) + slot;
             x.lo = max(0, q.gs - col * a.page);
             x.hi = min(a.page, q.ge - col * a.page);
           } else if (slot < q.n_pages) {
-            const int j = bk->blk[slot - q.n_gen];
+            const int j = blk_s[slot - q.n_gen];
             if (j >= 0 && j < a.table_cols && j * a.page < q.P) {
               col = j;
               x.hi = min(a.page, q.P - j * a.page);
@@ -590,36 +714,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
+        // what a tile's entry says, for all tiles of the batch at once: its pages are neighbouring
+        // lanes
+        auto finish = [&](Batch& x) {
+          x.vm = x.hi > x.lo ? fabsf(x.vs) : 0.f;
+          for (int off = 1; off < ppt; off <<= 1) x.vm = max_nan(x.vm, __shfl_xor_sync(0xffffffffu, x.vm, off));
+          x.f = x.vm == 0.f || x.hi <= x.lo ? 0.f : x.vs / x.vm * prob_top<FMT>();
+          x.part = __ballot_sync(0xffffffffu, x.lo > 0 || x.hi < a.page);
+        };
         if (SPARSE && lane == 0) {
           const long long g0 = a.g0[b];          // a current block that leaves the table
           if (g0 < 0 || g0 + a.G > static_cast<long long>(a.table_cols) * a.page) record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
         }
         if (!SPARSE && lane == 0 && a.lens[b] > a.table_cols * a.page) record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
-        int bbase = first * ppt;
+        const int j0 = n_tiles - first;          // the CTA's number of tile 0 of this unit
+        n_tiles += d.n;
+        const int mine_first = first + ((j0 + first + pw) & 1);      // this producer's first tile
+        int bbase = first << tp;
         Batch cur = look_up(bbase + lane);
         resolve(cur);
-        for (int tile = first; tile < last && ok;) {
-          const int b_end = min(last, (bbase + 32) / ppt);
-          Batch nxt{-1, 0, 0, -1, 0.f, 0.f};
+        int tile = mine_first;
+        for (; tile < last && ok;) {
+          const int b_end = min(last, (bbase + 32) >> tp);
+          Batch nxt{-1, 0, 0, -1, 0.f, 0.f, 0.f, 0.f, 0u};
           if (b_end < last) nxt = look_up(bbase + 32 + lane);
-          bool resolved = false;
-          int done = tile;                       // tiles whose scales are published
+          bool resolved = false, finished = false, cold = tile == mine_first;
+          int done = tile;                       // the next tile whose scales are to be published
           while (done < b_end && ok) {
-            // copies of every tile of the batch that finds a free stage, at least one
-            while (tile < b_end) {
-              const int s = issued % STAGES;
-              if (issued >= STAGES) {
-                const uint32_t ph = ((issued / STAGES) - 1) & 1;
+            // Copies of the next tile; at the start of a run, while its first scales are on their
+            // way, of as many as find a free stage (afterwards scales go with each tile, or they
+            // would hold up its use)
+            do {
+              const int j = j0 + tile, s = j % STAGES;
+              if (j >= STAGES) {
+                const uint32_t ph = ((j / STAGES) - 1) & 1;
                 bool got;
                 if (tile == done) {
-                  got = ok = __all_sync(0xffffffffu, mbar_wait(&bk->empty[s], ph, abort_flag, a.dev_err,
-                                                               DEV_ERR_TIMEOUT_PRODUCER));
+                  got = ok = wait_phase(&bk->empty[s], ph, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_PRODUCER);
                 } else {
                   got = __all_sync(0xffffffffu, mbar_test(&bk->empty[s], ph));
                 }
                 if (!got) break;
               }
-              const int rel = bbase + lane - tile * ppt;             // this lane's page of the tile
+              const int rel = bbase + lane - (tile << tp);           // this lane's page of the tile
               const bool mine = rel >= 0 && rel < ppt && cur.pg >= 0;
               const unsigned any = __ballot_sync(0xffffffffu, mine);
               if (lane == 0) mbar_arrive_expect_tx(&bk->full[s], static_cast<uint32_t>(__popc(any) * 2 * a.page * D));
@@ -636,29 +773,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               __syncwarp();
-              ++issued;
-              ++tile;
-            }
+              issued = j + 1;
+              tile += kProducers;
+            } while (cold && tile < b_end);
             if (!ok) break;
-            for (; done < tile; ++done) {
-              const int s = (issued - (tile - done)) % STAGES;
+            if (!finished) finish(cur);
+            cold = false;
+            finished = true;
+            for (; done < tile; done += kProducers) {
+              const int s = (j0 + done) % STAGES;
+              if (!SPARSE || done * 128 + 128 <= (q.n_pages << a.page_shift)) {
+                // whole pages: each lane its own, and each softmax thread looks up its key's
+                const int rel = bbase + lane - (done << tp);
+                if (rel >= 0 && rel < ppt)
+                  bk->page[s][rel] = make_float4(cur.ks, cur.f, __int_as_float(cur.lo), __int_as_float(cur.hi));
+                if (rel == 0) {
+                  bk->vmax[s] = cur.vm / prob_top<FMT>();
+                  bk->info[s] = (cur.part >> lane) & ((1u << ppt) - 1u) ? kMasked : 0;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bk->full[s]);
+                if (!resolved && b_end < last) {
+                  resolve(nxt);
+                  resolved = true;
+                }
+                continue;
+              }
+              if constexpr (SPARSE) {
               // keys 4 lane .. 4 lane + 3 lie in one page slot, or among the sinks
               const int k0 = done * 128 + 4 * lane;
-              const int slot = k0 / a.page, from = (slot - bbase) & 31;
+              const int slot = k0 >> a.page_shift, from = (slot - bbase) & 31, r = k0 & (a.page - 1);
+              const int lo = __shfl_sync(0xffffffffu, cur.lo, from), hi = __shfl_sync(0xffffffffu, cur.hi, from);
+              const float k = __shfl_sync(0xffffffffu, cur.ks, from), v = __shfl_sync(0xffffffffu, cur.vs, from);
               float ks[4], vs[4];
               bool on[4];
-              {
-                const int lo = __shfl_sync(0xffffffffu, cur.lo, from), hi = __shfl_sync(0xffffffffu, cur.hi, from);
-                const float k = __shfl_sync(0xffffffffu, cur.ks, from), v = __shfl_sync(0xffffffffu, cur.vs, from);
-                const int r = k0 - slot * a.page;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  on[e] = slot < q.n_pages && r + e >= lo && r + e < hi;
-                  ks[e] = on[e] ? k : 0.f;
-                  vs[e] = on[e] ? v : 0.f;
-                }
+              for (int e = 0; e < 4; ++e) {
+                on[e] = slot < q.n_pages && r + e >= lo && r + e < hi;
+                ks[e] = k;
+                vs[e] = on[e] ? v : 0.f;
               }
-              if (SPARSE && done * 128 + 128 > q.n_pages * a.page) {
+              {
                 if (n_snk < 0) {
                   // the sinks that no other slot holds: a sink is dropped inside the current
                   // block, inside a kept block, and when it was listed before
@@ -670,32 +825,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int prev = __shfl_up_sync(0xffffffffu, v, 1);
                     const int pv = lane == 0 ? before : prev;
                     up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i0 + lane > 0);
-                    if (i0 + lane < a.S) bk->snk[i0 + lane] = v;
+                    if (i0 + lane < a.S) snk_s[i0 + lane] = v;
                     before = __shfl_sync(0xffffffffu, v, 31);
                   }
                   up = __all_sync(0xffffffffu, up);
                   __syncwarp();
                   for (int i0 = (a.S - 1) & ~31; i0 >= 0; i0 -= 32) {
-                    const int i = i0 + lane, v = i < a.S ? bk->snk[i] : -1;
+                    const int i = i0 + lane, v = i < a.S ? snk_s[i] : -1;
                     bool drop = v < 0 || (v >= q.gs && v < q.ge);
                     if (!up)
-                      for (int j = 0; j < i && !drop; ++j) drop = bk->snk[j] == v;
+                      for (int j = 0; j < i && !drop; ++j) drop = snk_s[j] == v;
                     if (!drop && v < q.P) {
-                      const int col = v / a.page;
+                      const int col = v >> a.page_shift;
                       if (lists_sorted) {        // ascending, then -1
                         int lo = 0, hi = a.C;
                         while (lo < hi) {
-                          const int mid = (lo + hi) >> 1, x = bk->blk[mid];
+                          const int mid = (lo + hi) >> 1, x = blk_s[mid];
                           if (x >= 0 && x < col) lo = mid + 1;
                           else hi = mid;
                         }
-                        drop = lo < a.C && bk->blk[lo] == col;
+                        drop = lo < a.C && blk_s[lo] == col;
                       } else {
-                        for (int j = 0; j < a.C && !drop; ++j) drop = bk->blk[j] == col;
+                        for (int j = 0; j < a.C && !drop; ++j) drop = blk_s[j] == col;
                       }
                     }
                     __syncwarp();
-                    if (drop && i < a.S) bk->snk[i] = -1;
+                    if (drop && i < a.S) snk_s[i] = -1;
                     __syncwarp();
                   }
                   n_snk = a.S;
@@ -703,15 +858,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int i = k0 + e - q.n_pages * a.page;
-                  const int pos = i >= 0 && i < n_snk ? bk->snk[i] : -1;
+                  const int pos = i >= 0 && i < n_snk ? snk_s[i] : -1;
                   if (pos < 0) continue;
-                  const int pg = checked_page(a.table, a.table_cols, b, pos / a.page, a.n_pages, a.dev_err);
+                  const int pg = checked_page(a.table, a.table_cols, b, pos >> a.page_shift, a.n_pages, a.dev_err);
                   if (pg < 0) continue;
                   const long long ph = static_cast<long long>(pg) * a.Hkv + kvh;
                   on[e] = true;
                   ks[e] = __ldg(a.scale[0] + ph);
                   vs[e] = __ldg(a.scale[1] + ph);
-                  const long long off = (ph * a.page + pos % a.page) * D;
+                  const long long off = (ph * a.page + (pos & (a.page - 1))) * D;
                   const uint32_t dst = smem_u32(smem) + s * 2 * SM::kTile;
 #pragma unroll
                   for (int c = 0; c < D / 16; ++c) {
@@ -725,15 +880,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               float vm = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
               if (vs[0] != vs[0] || vs[1] != vs[1] || vs[2] != vs[2] || vs[3] != vs[3]) vm = NAN;
               vm = warp_max_nan(vm);
-              float2* key = &bk->key[s][4 * lane];
-              const float c = vm == 0.f ? 0.f : prob_top<FMT>();
+              // values relative to the tile's largest (four of a page are the same)
+              float f[4];
+              f[0] = vm == 0.f ? 0.f : vs[0] / vm * prob_top<FMT>();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) key[e] = make_float2(ks[e], vm == 0.f ? 0.f : vs[e] / vm * c);
+              for (int e = 1; e < 4; ++e)
+                f[e] = vs[e] == vs[0] ? f[0] : vm == 0.f ? 0.f : vs[e] / vm * prob_top<FMT>();
+              float4* key = reinterpret_cast<float4*>(&bk->key[s][4 * lane]);
+              key[0] = make_float4(ks[0], f[0], ks[1], f[1]);
+              key[1] = make_float4(ks[2], f[2], ks[3], f[3]);
               *reinterpret_cast<uchar4*>(&bk->valid[s][4 * lane]) = make_uchar4(on[0], on[1], on[2], on[3]);
-              const bool part = !__all_sync(0xffffffffu, on[0] && on[1] && on[2] && on[3]);
               if (lane == 0) {
                 bk->vmax[s] = vm / prob_top<FMT>();
-                bk->masked[s] = part ? 1 : 0;
+                bk->info[s] = kMasked | kByKey;
               }
               __syncwarp();
               if (lane == 0) mbar_arrive(&bk->full[s]);
@@ -741,8 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 resolve(nxt);
                 resolved = true;
               }
+              }
             }
           }
+          if (!resolved && b_end < last) resolve(nxt);
           cur = nxt;
           bbase += 32;
         }
@@ -754,306 +915,283 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       // a wait ran out: the copies under way still have to land before the CTA may leave
-      for (int j = max(0, issued - STAGES); j < issued; ++j) {
+      for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j -= kProducers) {
         const unsigned long long w0 = globaltimer();
         if (lane == 0) mbar_arrive(&bk->full[j % STAGES]);
-        while (!mbar_try_wait(&bk->full[j % STAGES], (j / STAGES) & 1) && globaltimer() - w0 < 500000000ull) {
+        while (!__all_sync(0xffffffffu, mbar_test(&bk->full[j % STAGES], (j / STAGES) & 1)) &&
+               !__any_sync(0xffffffffu, globaltimer() - w0 > 500000000ull)) {
         }
       }
     }
     __syncwarp();
-  } else if (warp == kMma) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp takes every step and one elected thread issues: the descriptors then stay
-    // in uniform registers. (Inside a branch on lane == 0 an MMA cost 110 cycles to issue, with
-    // the elected thread about 60.)
+  } else if (warp == kMmaS || warp == kMmaO) {
+    // ------------------------------------------------------------ MMA issuers
+    // A warp for each product, so that neither a late tile holds up a finished P nor the other
+    // way. The whole warp takes every step and one elected thread issues: the descriptors then
+    // stay in uniform registers. (Inside a branch on lane == 0 an MMA cost 110 cycles to issue,
+    // with the elected thread about 60.)
     const uint32_t elected = elect_one();
-    const uint32_t id_qk = idesc8<FMT>(2 * NQ, false), id_pv = idesc8<FMT>(2 * NQ, true);
+    const bool qk = warp == kMmaS;
+    const uint32_t id = idesc8<FMT>(2 * NQ, !qk);
     const uint64_t k0 = tile_desc<D>(smem_u32(smem));
     const uint64_t q0 = tile_desc<D>(smem_u32(smem) + SM::kQ);
     const uint64_t p0 = tile_desc<SM::kPRow>(smem_u32(smem) + SM::kP);
-    // QK runs ahead of PV by as many tiles as there are buffers of S^T; whichever product has its
-    // operands goes next, so that neither a late tile holds up a finished P nor the other way.
-    int di = -1, left = 0;                 // descriptor, tiles left in it
-    int j_qk = 0, j_pv = 0;                // next tile of either product
-    bool ended = false, fresh = false;     // no more tiles; the run's queries are still to come
-    auto test = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
-    unsigned long long idle = 0;           // since when neither could go on
-    while (!ended || j_pv < j_qk) {
-      bool did = false;
-      if (!ended && left == 0 && test(&bk->d_full[(di + 1) % kDescs], ((di + 1) / kDescs) & 1)) {
-        if (di >= 0 && lane == 0) mbar_arrive(&bk->d_empty[di % kDescs]);
-        ++di;
-        left = bk->desc[di % kDescs].n;
-        __syncwarp();
-        ended = left == 0;
-        fresh = true;
-        did = true;
-      }
-      const int s = j_qk % STAGES;
-      if (left > 0 && j_qk - j_pv < SM::kS && (!fresh || test(&bk->q_full[di & 1], (di >> 1) & 1)) &&
-          test(&bk->full[s], (j_qk / STAGES) & 1)) {
-        tc_fence_after();
-        const int qb = di & 1, sb = j_qk % SM::kS;
-        const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
-        const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
-        fresh = false;
-        --left;
-        if (elected) {
-#pragma unroll
-          for (int ks = 0; ks < D / 32; ++ks)
-            mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id_qk, ks > 0 ? 1u : 0u);
-          mma_commit(&bk->s_full[sb]);
-          if (left == 0) mma_commit(&bk->q_empty[qb]);
-        }
-        __syncwarp();
-        ++j_qk;
-        did = true;
-      }
-      const int buf = j_pv & 1;
-      if (j_pv < j_qk && test(&bk->p_full[buf], (j_pv >> 1) & 1)) {
-        tc_fence_after();
-        const int sv = j_pv % STAGES;
-        const uint64_t vd = k0 + static_cast<uint64_t>((sv * 2 + 1) * SM::kTile / 16);
-        const uint64_t pd = p0 + static_cast<uint64_t>(buf * SM::kPBuf / 16);
-        if (elected) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma8<FMT>(tO + buf * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id_pv, ks > 0 ? 1u : 0u);
-          mma_commit(&bk->o_full[buf]);
-          mma_commit(&bk->empty[sv]);
-        }
-        __syncwarp();
-        ++j_pv;
-        did = true;
-      }
-      if (did) {
-        idle = 0;
-      } else {
-        const unsigned long long now = globaltimer();
-        if (idle == 0) idle = now;
-        bool stop = *abort_flag != 0;
-        if (now - idle > kWaitLimitNs) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            record_dev_error(a.dev_err, DEV_ERR_TIMEOUT_MMA);
-          }
-          stop = true;
-        }
-        if (__any_sync(0xffffffffu, stop)) break;
-      }
-    }
-    if (elected) mma_commit(&bk->drain);
-    __syncwarp();
-    const unsigned long long w0 = globaltimer();
-    while (!mbar_try_wait(&bk->drain, 0) && globaltimer() - w0 < 500000000ull) {
-    }
-    __syncwarp();
-  } else if (warp >= kQuery) {
-    // ------------------------------------------------------------ query rows
     bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      return ok = wait_phase(bar, parity, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA);
+    };
+    int j = 0;
     for (int di = 0; ok; ++di) {
       const int ds = di % kDescs, qb = di & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bk->d_full[ds], (di / kDescs) & 1, abort_flag, a.dev_err,
-                                             DEV_ERR_TIMEOUT_PRODUCER));
-      if (!ok) break;
+      if (!wait(&bk->d_full[ds], (di / kDescs) & 1)) break;
       const Desc d = bk->desc[ds];
+      const int n = d.n;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk->d_empty[ds]);
-      if (d.n == 0) break;
-      if (di >= 2)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1, abort_flag, a.dev_err,
-                                               DEV_ERR_TIMEOUT_PRODUCER));
-      if (!ok) break;
-      // the first run's rows are shared with the softmax warps, which have nothing else to do yet
-      split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], warp - kQuery, di == 0 ? 10 : 2);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_n(&bk->q_full[qb], di == 0 ? 1 : 5);
+      if (n == 0) break;
+      if (qk) {
+        // the run's query rows: the first run's shared with the softmax warps, which have nothing
+        // else to do yet, later ones' ahead of those warps by the buffers of S^T
+        if (di >= 2 && !wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1)) break;
+        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], 0, di == 0 ? kQParts : 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&bk->q_full[qb], di == 0 ? 1 : kQParts);
+        if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
+      }
+      for (const int je = j + n; j < je; ++j) {
+        const int s = j % STAGES;
+        if (qk) {
+          const int sb = j % Sp::kS;
+          if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
+          if (j >= Sp::kS && !wait(&bk->s_free[sb], (j / Sp::kS - 1) & 1)) break;
+          tc_fence_after();
+          const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
+          const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
+          if (elected) {
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks)
+              mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id, ks > 0 ? 1u : 0u);
+            mma_commit(&bk->s_full[sb]);
+            if (j == je - 1) mma_commit(&bk->q_empty[qb]);
+            mbar_arrive(&bk->s_full[sb]);
+          }
+        } else {
+          const int buf = j % Sp::kBuf;
+          if (!wait(&bk->p_full[buf], (j / Sp::kBuf) & 1)) break;
+          if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
+          tc_fence_after();
+          const uint64_t vd = k0 + static_cast<uint64_t>((s * 2 + 1) * SM::kTile / 16);
+          const uint64_t pd = p0 + static_cast<uint64_t>(buf * SM::kPBuf / 16);
+          if (elected) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma8<FMT>(tO + buf * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id, ks > 0 ? 1u : 0u);
+            mma_commit(&bk->o_full[buf]);
+            mma_commit(&bk->empty[s]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // (after a wait that ran out, products may still be under way)
+    if (elected) mma_commit(&bk->drain[qk ? 0 : 1]);
+    __syncwarp();
+    const unsigned long long w0 = globaltimer();
+    while (!__all_sync(0xffffffffu, mbar_test(&bk->drain[qk ? 0 : 1], 0)) &&
+           !__any_sync(0xffffffffu, globaltimer() - w0 > 500000000ull)) {
     }
   } else {
     // ------------------------------------------------------------ softmax groups
     const int grp = warp >> 2, wq = warp & 3;
     const int t = threadIdx.x & 127;             // key of the tile == TMEM lane == dim of O^T
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const int c0 = kBoth ? grp * 32 : 0;         // first column
+    const int slot = grp / Sp::kPer;             // tiles j with j % kSlots == slot
+    const int c0 = grp % Sp::kPer * NC;          // first column
     const int bar = 1 + grp;
-    const int lc = lane < NC ? lane : 0;         // the column whose maximum this lane follows
+    const int lc = lane & (NC - 1);              // the column that this lane follows (the same in all warps)
     bool ok = true;
     int n_x = 0;                                 // exchanges so far
     int par = 0;
-    // A warp whose wait ran out goes on without waits or tensor memory to the next barrier of its
-    // group, where the whole group leaves: the four warps always take the same barriers.
+    // A warp whose wait ran out goes on without waits or tensor memory to the end of the run, where
+    // the whole group leaves: its four warps always take the same barriers.
+    auto wait = [&](uint64_t* bar_, int parity) {
+      if (ok) ok = wait_phase(bar_, parity, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_SOFTMAX);
+    };
     for (int di = 0;; ++di) {
       const int ds = di % kDescs, qb = di & 1;
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->d_full[ds], (di / kDescs) & 1, abort_flag, a.dev_err,
-                                               DEV_ERR_TIMEOUT_SOFTMAX));
+      wait(&bk->d_full[ds], (di / kDescs) & 1);
       Desc d{};
       if (ok) d = bk->desc[ds];
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bk->d_empty[ds]);
-      if (ok && d.n > 0 && di == 0) {
-        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 2 + warp, 10);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bk->q_full[0]);
+      if (ok && d.n > 0) {
+        if (di == 0) {
+          split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 1 + warp, kQParts);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->q_full[0]);
+        }
+        wait(&bk->q_full[qb], (di >> 1) & 1);
       }
-      if (ok && d.n > 0)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->q_full[qb], (di >> 1) & 1, abort_flag, a.dev_err,
-                                               DEV_ERR_TIMEOUT_SOFTMAX));
       if (bar_red_or(bar, 128, !ok) || d.n == 0) break;      // the whole group leaves together
       // (a zero query or scale: with the smallest normal number instead, every finite score is
       // still 0, and a masked key's -infinity stays what it is)
-      const float qs_read = bk->q_scale[qb][c0 + lc];
-      const float qs = qs_read == 0.f ? 1.17549435e-38f : qs_read;
+      auto no_zero = [](float v) { return v == 0.f ? 1.17549435e-38f : v; };
+      const float qs = no_zero(bk->q_scale[qb][c0 + lc]);              // of the column this lane follows
+      if (lane < NC) bk->qs[warp][lane] = qs;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
-      // Sums over tiles are relative to 2^m_ref, which is the largest score of the run's first
-      // tile and moves up only when another tile's is 2^30 times as large: fp32 has the range, and
-      // no sum is rescaled tile by tile.
-      float acc[NC], lsum[NC], m_ref = -INFINITY;
+      // A tile's probabilities are relative to a reference of its own, the next whole number (that
+      // bf16 holds) above its largest score in units of log2. (Against a running maximum instead,
+      // all that lies 2^-18 below one large key, an attention sink, would be rounded away, and with
+      // thousands of such keys a part of the result; so, no more than 128 * 2^-18 of a tile's own
+      // largest is, or 2^-17.) Sums over tiles are relative to m_ref, the reference of the run's
+      // first tile with keys, which moves up only when another is above it by 30: fp32 has the
+      // range, no sum is rescaled tile by tile, and the factor between the two is an exact power of
+      // two. Whole numbers make both 16 bits wide: handing them from a column's lane to all
+      // threads costs shared-memory bandwidth, of which the tensor cores take half.
+      float2 acc[NC / 2], lsum[NC / 2];
+      uint32_t be2[NC / 2] = {};                 // factors of the group's last tile (pairs of bf16)
+      float be_v = 0.f;                          // and its value scale
+      float m_ref = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NC; ++n) acc[n] = lsum[n] = 0.f;
+      for (int n = 0; n < NC / 2; ++n) acc[n] = lsum[n] = make_float2(0.f, 0.f);
       // adds O^T of tile j, in its buffer, to the sums
       auto collect = [&](int j) {
-        const int buf = j & 1;
-        if (ok)
-          ok = __all_sync(0xffffffffu, mbar_wait(&bk->o_full[buf], (j >> 1) & 1, abort_flag, a.dev_err,
-                                                 DEV_ERR_TIMEOUT_SOFTMAX));
+        const int buf = j % Sp::kBuf;
+        wait(&bk->o_full[buf], (j / Sp::kBuf) & 1);
         if (!ok) return;
         tc_fence_after();
-        uint32_t r[NC], r2[NC];
-        tmem_ld_cols<NC>(tO + buf * SM::kAcc + lane_addr + c0, r);
-        tmem_ld_cols<NC>(tO + buf * SM::kAcc + NQ + lane_addr + c0, r2);
-        tmem_ld_wait();
-        const float4* f = reinterpret_cast<const float4*>(bk->post[warp][buf]);
 #pragma unroll
-        for (int n = 0; n < NC; n += 4) {
-          const float4 v = f[n / 4];
-          acc[n] += v.x * both<FMT>(r[n], r2[n]);
-          acc[n + 1] += v.y * both<FMT>(r[n + 1], r2[n + 1]);
-          acc[n + 2] += v.z * both<FMT>(r[n + 2], r2[n + 2]);
-          acc[n + 3] += v.w * both<FMT>(r[n + 3], r2[n + 3]);
+        for (int h = 0; h < NC; h += 8) {
+          uint32_t r[8], r2[8];
+          tmem_ld8(tO + buf * SM::kAcc + lane_addr + c0 + h, r);
+          tmem_ld8(tO + buf * SM::kAcc + NQ + lane_addr + c0 + h, r2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float2 o = mul2(both2<FMT>(r + 2 * n, r2 + 2 * n), make_float2(be_v, be_v));
+            acc[h / 2 + n] = fma2(bf16_pair(be2[h / 2 + n]), o, acc[h / 2 + n]);
+          }
         }
         tc_fence_before();
       };
       const int jb = d.j0, je = d.j0 + d.n;
-      constexpr int kStep = kBoth ? 1 : 2;
-      const int j_first = kBoth ? jb : jb + ((jb ^ grp) & 1);
-      bool left_early = false;
-      for (int j = j_first; j < je; j += kStep) {
-        const int buf = j & 1, s = j % STAGES, sb = j % SM::kS;
-        if (j - 2 >= jb) collect(j - 2);
-        if (ok)
-          ok = __all_sync(0xffffffffu, mbar_wait(&bk->full[s], (j / STAGES) & 1, abort_flag, a.dev_err,
-                                                 DEV_ERR_TIMEOUT_SOFTMAX));
-        float2 key = make_float2(0.f, 0.f);
-        bool on = true, masked = false;
-        float vmax = 0.f;
-        if (ok) {
-          key = bk->key[s][t];
-          masked = bk->masked[s] != 0;
-          vmax = bk->vmax[s];
-          if (masked) on = bk->valid[s][t] != 0;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bk->s_full[sb], (j / SM::kS) & 1, abort_flag, a.dev_err,
-                                                 DEV_ERR_TIMEOUT_SOFTMAX));
+      const int j_first = jb + (slot - jb % Sp::kSlots + Sp::kSlots) % Sp::kSlots;
+      int s = j_first % STAGES;
+      for (int j = j_first; j < je; j += Sp::kSlots) {
+        const int buf = j % Sp::kBuf, sb = j % Sp::kS;
+        wait(&bk->s_full[sb], (j / Sp::kS) & 1);   // (and with it the tile's scales and bytes)
+        const int info = bk->info[s];
+        const float4 pg = bk->page[s][t >> a.page_shift];
+        const float vmax = bk->vmax[s];
+        float2 key = make_float2(pg.x, pg.y);
+        bool off = false;                        // this thread's key is masked
+        if (info != 0) {
+          asm volatile("" ::: "memory");         // (a branch: few tiles come here)
+          if (info & kByKey) {
+            key = bk->key[s][t];
+            off = bk->valid[s][t] == 0;
+          } else {
+            const int r = t & (a.page - 1);
+            off = r < __float_as_int(pg.z) || r >= __float_as_int(pg.w);
+          }
         }
-        float x[NC];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) x[n] = 0.f;
+        float2 x[NC / 2];
         if (ok) {
           tc_fence_after();
-          uint32_t r[NC], r2[NC];
-          tmem_ld_cols<NC>(tS + sb * SM::kAcc + lane_addr + c0, r);
-          tmem_ld_cols<NC>(tS + sb * SM::kAcc + NQ + lane_addr + c0, r2);
-          tmem_ld_wait();
 #pragma unroll
-          for (int n = 0; n < NC; ++n) x[n] = both<FMT>(r[n], r2[n]) * key.x;
+          for (int h = 0; h < NC; h += 16) {
+            uint32_t r[16], r2[16];
+            tmem_ld16(tS + sb * SM::kAcc + lane_addr + c0 + h, r);
+            tmem_ld16(tS + sb * SM::kAcc + NQ + lane_addr + c0 + h, r2);
+            tmem_ld_wait();
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[h / 2 + n] = mul2(both2<FMT>(r + 2 * n, r2 + 2 * n), make_float2(key.x, key.x));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->s_free[sb]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NC / 2; ++n) x[n] = make_float2(0.f, 0.f);
         }
-        if (masked && !on) {
+        if (info != 0) {
+          asm volatile("" ::: "memory");
 #pragma unroll
-          for (int n = 0; n < NC; ++n) x[n] = -INFINITY;
+          for (int n = 0; n < NC / 2; ++n)
+            x[n] = make_float2(off ? -INFINITY : x[n].x, off ? -INFINITY : x[n].y);
         }
         // the largest of each column: over the warp, then over the group's four warps; lane n of
         // every warp follows column n
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const float m = warp_max_nan(x[n]);
-          top[n & 3] = lane == n ? m : top[n & 3];
-        }
-        const float mine = (lane & 2) ? ((lane & 1) ? top[3] : top[2]) : ((lane & 1) ? top[1] : top[0]);
         par ^= 1;
-        if (lane < NC) bk->red[grp][par][wq][lane] = mine;
-        if (bar_red_or(bar, 128, !ok)) {
-          left_early = true;
-          break;
-        }
-        {
-          const float* rd = &bk->red[grp][par][0][0];
-          const float mt = max_nan(max_nan(rd[lc], rd[32 + lc]), max_nan(rd[64 + lc], rd[96 + lc]));
-          const float ms = mt == -INFINITY ? -INFINITY : mt * qs;      // in units of log2
-          // The tile's probabilities are relative to its own largest score. Against the running
-          // maximum instead, all that lies 2^-18 below one large key (an attention sink) would be
-          // rounded away, and with thousands of such keys a part of the result; so, no more than
-          // 128 * 2^-18 of a tile's own largest is.
-          float al = 1.f;
-          if (ms > m_ref + 30.f || (m_ref == -INFINITY && ms > -INFINITY)) {
-            al = exp2_approx(m_ref - ms);
-            m_ref = ms;
-          }
-          const float be = ms == -INFINITY ? 0.f : exp2_approx(ms - m_ref);
-          __syncwarp();                                                // the last tile's factors have been read
-          if (__any_sync(0xffffffffu, al != 1.f)) {                    // the same in the group's four warps
-            if (lane < NC) {
-              bk->be[warp][lane] = al;
-              bk->post[warp][buf ^ 1][lane] *= al;                     // a product that is still under way
-            }
-            __syncwarp();
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-              const float f = bk->be[warp][n];
-              lsum[n] *= f;
-              acc[n] *= f;
+        for (int n = 0; n < NC; n += 4) {
+          float4 m;
+          m.x = warp_max_nan(x[n / 2].x);
+          m.y = warp_max_nan(x[n / 2].y);
+          m.z = warp_max_nan(x[n / 2 + 1].x);
+          m.w = warp_max_nan(x[n / 2 + 1].y);
+          if (lane == 0) *reinterpret_cast<float4*>(&bk->red[grp][par][wq][n]) = m;
+        }
+        // The buffers of P and O^T are free once the product that used them has been added, which
+        // was under way while this tile's scores were formed
+        if (j - Sp::kBuf >= jb) collect(j - Sp::kBuf);
+        named_bar_sync(bar, 128);
+        float ref = 0.f, fe;
+        {
+          const float* rl = &bk->red[grp][par][0][0];
+          const float mt = max3_nan(max_nan(rl[lc], rl[NC + lc]), rl[2 * NC + lc], rl[3 * NC + lc]);
+          uint32_t r16 = 0;                      // bf16 of the reference
+          float al = 1.f;
+          fe = 0.f;
+          if (mt != -INFINITY) {                 // (a tile without keys adds nothing)
+            const uint32_t c = __float_as_uint(ceilf(mt * qs));
+            r16 = mt != mt ? 0x7fc0u : (c & 0x80000000u) ? c >> 16 : (c + 0xffffu) >> 16;
+            ref = __uint_as_float(r16 << 16);
+            if (ref > m_ref + 30.f || m_ref == -INFINITY) {
+              al = exp2_approx(m_ref - ref);
+              m_ref = ref;
             }
-            __syncwarp();
+            fe = exp2_approx(ref - m_ref);
           }
           if (lane < NC) {
-            bk->pre[warp][lane] = make_float2(qs, ms == -INFINITY ? 0.f : -ms);
-            bk->be[warp][lane] = be;
-            bk->post[warp][buf][lane] = be * vmax;
+            bk->ref[warp][lane] = static_cast<uint16_t>(r16 ^ 0x8000u);
+            bk->be[warp][lane] = static_cast<uint16_t>(__float_as_uint(fe) >> 16);
+          }
+          if (__any_sync(0xffffffffu, al != 1.f)) {                    // the same in the group's four warps
+#pragma unroll
+            for (int n = 0; n < NC / 2; ++n) {
+              const float2 f = make_float2(__shfl_sync(0xffffffffu, al, 2 * n), __shfl_sync(0xffffffffu, al, 2 * n + 1));
+              lsum[n] = mul2(lsum[n], f);
+              acc[n] = mul2(acc[n], f);
+            }
           }
           __syncwarp();
         }
-        const float4* pre = reinterpret_cast<const float4*>(bk->pre[warp]);
-        const float4* pbe = reinterpret_cast<const float4*>(bk->be[warp]);
         // P is written as it is held, a key to a row, hi then lo: an MN-major operand. (Stored
         // query-major, a byte at a time, the stores alone took 1500 cycles of a tile.)
         uint8_t* pbuf = smem + SM::kP + buf * SM::kPBuf;
 #pragma unroll
-        for (int n0 = 0; n0 < NC; n0 += 16) {
+        for (int h = 0; h < NC; h += 16) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 4 * i;
-            const float4 e0 = pre[n / 2], e1 = pre[n / 2 + 1], be = pbe[n / 4];
-            float p[4];
-            p[0] = exp2_approx(x[n] * e0.x + e0.y);
-            p[1] = exp2_approx(x[n + 1] * e0.z + e0.w);
-            p[2] = exp2_approx(x[n + 2] * e1.x + e1.y);
-            p[3] = exp2_approx(x[n + 3] * e1.z + e1.w);
-            lsum[n] += p[0] * be.x;
-            lsum[n + 1] += p[1] * be.y;
-            lsum[n + 2] += p[2] * be.z;
-            lsum[n + 3] += p[3] * be.w;
-            split4<FMT>(p, key.y, hi[i], lo[i]);
+            const int n = h + 4 * i;
+            const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[warp][n]);
+            const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[warp][n]);
+            const float2 v0 = fma2(x[n / 2], make_float2(qv.x, qv.y), bf16_pair(rv.x));
+            const float2 v1 = fma2(x[n / 2 + 1], make_float2(qv.z, qv.w), bf16_pair(rv.y));
+            x[n / 2] = make_float2(exp2_approx(v0.x), exp2_approx(v0.y));
+            x[n / 2 + 1] = make_float2(exp2_approx(v1.x), exp2_approx(v1.y));
+            split4<FMT>(mul2(x[n / 2], make_float2(key.y, key.y)), mul2(x[n / 2 + 1], make_float2(key.y, key.y)), hi[i], lo[i]);
           }
-          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (c0 + n0) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (NQ + c0 + n0) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (c0 + h) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (NQ + c0 + h) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         // A masked key's values may be anything, NaN codes included, and 0 * NaN is NaN
-        if (FMT == FOCUS_CACHE_E4M3 && masked && !on && (!kBoth || grp == 0)) {
+        if (FMT == FOCUS_CACHE_E4M3 && off && c0 == 0) {
           uint8_t* v = smem + (s * 2 + 1) * SM::kTile;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + row_chunk<D>(t, c)) = make_uint4(0u, 0u, 0u, 0u);
@@ -1062,73 +1200,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bk->p_full[buf]);
-      }
-      if (left_early) break;
-      // the products still under way: of this group's last tile, or of the last two
-      {
-        const int lastj = kBoth ? je - 1 : je - 1 - ((je - 1 - j_first) & 1);
-        if (kBoth) {
-          if (je - 2 >= jb) collect(je - 2);
-          collect(je - 1);
-        } else if (lastj >= j_first) {
-          collect(lastj);
+        // while the product is under way: the tile's row sums, and its factors for O^T
+        be_v = vmax;
+#pragma unroll
+        for (int h = 0; h < NC / 8; ++h) {
+          const uint4 w = reinterpret_cast<const uint4*>(bk->be[warp])[h];
+          be2[4 * h] = w.x;
+          be2[4 * h + 1] = w.y;
+          be2[4 * h + 2] = w.z;
+          be2[4 * h + 3] = w.w;
         }
+#pragma unroll
+        for (int n = 0; n < NC / 2; ++n) lsum[n] = fma2(x[n], bf16_pair(be2[n]), lsum[n]);
+        __syncwarp();
+        s += Sp::kSlots;
+        if (s >= STAGES) s -= STAGES;
       }
+      // the product still under way
+      if (j_first < je) collect(je - 1 - (je - 1 - j_first) % Sp::kSlots);
       // row sums over the 128 keys
       float l;
       {
+        float ls[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) ls[n] = n & 1 ? lsum[n / 2].y : lsum[n / 2].x;
         if constexpr (NC == 32) {
-          warp_sum_scatter<32>(lsum);
-          l = lsum[0];
+          warp_sum_scatter<32>(ls);              // column n in lane n
+          l = ls[0];
         } else {
-          warp_sum_scatter16(lsum);
-          l = __shfl_sync(0xffffffffu, lsum[0], (2 * lane) & 31);
+          warp_sum_scatter16(ls);                // column n in lane 2 n
+          l = __shfl_sync(0xffffffffu, ls[0], (2 * lane) & 31);
         }
         par ^= 1;
         if (lane < NC) bk->red[grp][par][wq][lane] = l;
         if (bar_red_or(bar, 128, !ok)) break;
         const float* rd = &bk->red[grp][par][0][0];
-        l = (rd[lc] + rd[32 + lc]) + (rd[64 + lc] + rd[96 + lc]);
+        l = (rd[lc] + rd[NC + lc]) + (rd[2 * NC + lc] + rd[3 * NC + lc]);
       }
-      // Up to 32 rows: each group hands the other half of the columns over through the P
-      // buffers, which no product reads any more once both groups have collected theirs.
-      int n0 = 0;
-      if constexpr (!kBoth) {
-        constexpr int HC = NC / 2;
-        float* xch = reinterpret_cast<float*>(smem + SM::kP);        // [group][HC][128]
-        static_assert(2 * HC * 128 * 4 <= 2 * SM::kPBuf, "exchange exceeds the P buffers");
-        // both groups are past their last product
+      // Groups of the same columns: each puts out a part of them and gets the others' sums for
+      // these through the P buffers, which no product reads any more once all groups have
+      // collected theirs.
+      auto sum_of = [&](int n) { return n & 1 ? acc[n / 2].y : acc[n / 2].x; };
+      constexpr int OC = NC / Sp::kSlots;        // columns that a group puts out
+      const int n0 = slot * OC;
+      float out[OC];
+      if constexpr (Sp::kSlots > 1) {
         if (lane == 0) mbar_arrive(&bk->x_full);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->x_full, (2 * n_x) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_EPILOGUE));
+        wait(&bk->x_full, 0);
         if (bar_red_or(bar, 128, !ok)) break;
+        float* xch = reinterpret_cast<float*>(smem + SM::kP);        // [group of the sums][other's rank][OC][128]
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          const float v = grp == 0 ? acc[HC + i] : acc[i];
-          xch[(grp * HC + i) * 128 + t] = v;
+        for (int o = 0; o < Sp::kSlots; ++o) {
+          if (o == slot) continue;
+          // group (o, c0) reads this group's sums of its columns as its source number (slot - o - 1)
+          const int to = o * Sp::kPer + grp % Sp::kPer, rank = (slot - o - 1 + Sp::kSlots) % Sp::kSlots;
+#pragma unroll
+          for (int i = 0; i < OC; ++i) xch[((to * (Sp::kSlots - 1) + rank) * OC + i) * 128 + t] = sum_of(o * OC + i);
         }
         if (wq == 0 && lane < NC) bk->xml[grp][lane] = make_float2(m_ref, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bk->x_full);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->x_full, (2 * n_x + 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_EPILOGUE));
+        wait(&bk->x_full, 1);
         if (bar_red_or(bar, 128, !ok)) break;
-        const float2 om = bk->xml[1 - grp][lc];
-        const float M = max_nan(m_ref, om.x);
-        const float ca = l == 0.f ? 0.f : exp2_approx(m_ref - M), cb = om.y == 0.f ? 0.f : exp2_approx(om.x - M);
-        l = ca * l + cb * om.y;
-        m_ref = M;
-        n0 = grp * HC;
+        float M = m_ref;
+        float2 om[Sp::kSlots - 1];
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          const float fa = __shfl_sync(0xffffffffu, ca, n0 + i), fb = __shfl_sync(0xffffffffu, cb, n0 + i);
-          const float v = grp == 0 ? acc[i] : acc[HC + i];
-          acc[i] = fa * v + fb * xch[((1 - grp) * HC + i) * 128 + t];
+        for (int r = 0; r < Sp::kSlots - 1; ++r) {
+          om[r] = bk->xml[(slot + 1 + r) % Sp::kSlots * Sp::kPer + grp % Sp::kPer][lc];
+          M = max_nan(M, om[r].x);
         }
+        const float f0 = l == 0.f ? 0.f : exp2_approx(m_ref - M);
+        l *= f0;
+#pragma unroll
+        for (int i = 0; i < OC; ++i) {
+          float mine = sum_of(i);
+#pragma unroll
+          for (int o = 1; o < Sp::kSlots; ++o) mine = slot == o ? sum_of(o * OC + i) : mine;
+          out[i] = __shfl_sync(0xffffffffu, f0, n0 + i) * mine;
+        }
+#pragma unroll
+        for (int r = 0; r < Sp::kSlots - 1; ++r) {
+          const float f = om[r].y == 0.f ? 0.f : exp2_approx(om[r].x - M);
+          l += f * om[r].y;
+#pragma unroll
+          for (int i = 0; i < OC; ++i)
+            out[i] += __shfl_sync(0xffffffffu, f, n0 + i) * xch[((grp * (Sp::kSlots - 1) + r) * OC + i) * 128 + t];
+        }
+        m_ref = M;
+        __syncwarp();
         if (lane == 0) mbar_arrive(&bk->x_done);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bk->x_done, n_x & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_EPILOGUE));
+        wait(&bk->x_done, n_x & 1);
         ++n_x;
+      } else {
+#pragma unroll
+        for (int i = 0; i < OC; ++i) out[i] = sum_of(i);
       }
-      // out: columns n0 .. of the slice
-      constexpr int OC = kBoth ? NC : NC / 2;
+      // out: columns c0 + n0 .. of the slice
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
       for (int i = 0; i < OC; ++i) {
@@ -1136,11 +1303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = __shfl_sync(0xffffffffu, inv, n0 + i);
         if (n < d.rows && t < D) {
           if (d.slot >= 0) {
-            a.part_o[(static_cast<size_t>(d.slot) * NQ + n) * D + t] = acc[i];
+            a.part_o[(static_cast<size_t>(d.slot) * NQ + n) * D + t] = out[i];
           } else {
             const int r = d.row0 + n, qh = r / a.qcap, qi = r - qh * a.qcap;
             const size_t row = (static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi;
-            a.O[row * D + t] = __float2bfloat16_rn(qi < d.nq ? acc[i] * f : 0.f);
+            a.O[row * D + t] = __float2bfloat16_rn(qi < d.nq ? out[i] * f : 0.f);
           }
         }
       }
@@ -1152,7 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMma) tmem_dealloc(tmem, SM::kTmem);
+  if (warp == kMmaS) tmem_dealloc(tmem, SM::kTmem);
 }
 
 // Joins the parts of the units that several CTAs worked on (a warp per query row, a lane holds
@@ -1179,9 +1346,9 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnArgs 
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   float l = 0.f;
   if (q.tiles > 0) {
-    const int T = tiles_of_all<SPARSE>(a) * heads;
+    const int T = length_of_all<SPARSE>(a) * heads;
     const int shares = min(a.grid, T);
-    const int x0 = tiles_before<SPARSE>(a, b) * heads + (kvh * a.n_slices + slice) * q.tiles;
+    const int x0 = length_before<SPARSE>(a, b) * heads + (kvh * a.n_slices + slice) * unit_length(q.tiles) + kLead;
     const int s0 = share_of(x0, T, shares), s1 = share_of(x0 + q.tiles - 1, T, shares);
     if (s0 == s1) return;
     float M = -INFINITY;
@@ -1306,7 +1473,7 @@ int run_cache_attention(CacheAttnArgs a, const focus_cache* c, void* ws, cudaStr
   // tiles at most, for the grid and for the 32-bit tile numbers
   const long long per_unit = SPARSE ? (static_cast<long long>((a.G + a.page - 2) / a.page + 1 + a.C) * a.page + a.S + 127) / 128
                                     : (static_cast<long long>(a.table_cols) * a.page + 127) / 128;
-  const long long most = static_cast<long long>(a.B) * a.Hkv * a.n_slices * per_unit;
+  const long long most = static_cast<long long>(a.B) * a.Hkv * a.n_slices * (per_unit + kLead);
   if (most >= (1LL << 31) || static_cast<long long>(a.B) * a.Hkv * rows >= (1LL << 32)) {
     set_error("cache attention: %lld tiles of 128 keys in one call", most);
     return FOCUS_ERR_UNSUPPORTED;
@@ -1358,6 +1525,7 @@ CacheAttnArgs attn_args(const focus_bf16* Q, const int32_t* n_q, const focus_cac
   a.table_cols = table_cols;
   a.n_pages = c->n_pages;
   a.page = c->page;
+  a.page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
   a.B = B;
   a.Hq = Hq;
   a.Hkv = c->Hkv;
