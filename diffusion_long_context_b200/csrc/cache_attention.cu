@@ -29,13 +29,17 @@
 // writes zeros for the units without keys. So one long sequence among short ones still fills
 // the GPU, and a sequence's length is only read on the device.
 //
-// Warps: 0-3 and 4-7 two softmax groups, 8 and 9 producers, a tile each in turn (TMA for pages,
-// cp.async for sink rows), 10 and 11 issue the products S^T and O^T (10 owns tensor memory and
-// prepares the query rows). A softmax thread owns a key and up to 32 query columns. Up to 32 query
-// rows the two groups take tiles in turn and join their sums at the end of a unit; with 64 rows
-// both work on every tile, 32 columns each. Twelve warps leave 168 registers to a thread: with four
-// groups of 16 columns (20 warps, 96 registers) the sums spilled, and a spilled register costs
-// 500 cycles beside a shared memory that leaves no L1.
+// A tile goes through a chain of warps, each of which works on a tile of its own, so that four
+// tiles or more are under way and the latencies of the hand-overs (mbarriers, tensor memory,
+// shuffles: half of a tile's way) are covered by the other tiles:
+//   16, 17  producers, a tile each in turn (TMA for pages, cp.async for sink rows)
+//   18      issues S^T = K Q^T (and prepares the query rows, and owns tensor memory)
+//   0-3     the largest score of every column in each warp's 32 keys, and warp 0 the references
+//   4-11    two groups, a tile each in turn: exp, row sums, hi and lo of P
+//   19      issues O^T = V^T P^T
+//   12-15   sum of O^T over tiles; at the end of a unit, the output
+// With one group taking a tile from its scores to its sum, and two such groups, a tile took 2200
+// cycles, most of them latency; the memory brings one every 1370.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -47,7 +51,8 @@
 namespace focus {
 namespace {
 
-constexpr int kSoftmaxWarps = 8;
+constexpr int kMaxWarp = 0, kExpWarp = 4, kSumWarp = 12;      // first warps of the stages
+constexpr int kSoftmaxWarps = 16;
 constexpr int kProducers = 2;
 constexpr int kProducer = kSoftmaxWarps, kMmaS = kProducer + kProducers, kMmaO = kMmaS + 1;
 constexpr int kThreads = (kMmaO + 1) * 32;
@@ -148,62 +153,52 @@ struct Desc {               // a run of tiles of one unit that this CTA works on
   int slot;                 // where the partial result goes, -1 = straight into O
 };
 
-// How a tile's NQ query columns are spread over the groups, and what is buffered.
-template <int NQ>
-struct Split {
-  static constexpr int kC = NQ < 32 ? NQ : 32;         // query columns of a softmax thread
-  static constexpr int kPer = NQ / kC;                 // groups of a tile
-  static constexpr int kSlots = 2 / kPer;              // tiles worked on in turn
-  static constexpr int kBuf = kSlots;                  // buffers of P and O^T
-  static constexpr int kS = 2 * kBuf;                  // buffers of S^T
-  static constexpr int kStages = NQ == 64 ? 4 : 5;
-};
+constexpr int kStages = 5;              // tiles in the K/V ring
+constexpr int kS = 3;                   // buffers of S^T, and of O^T
 
 template <int NQ>
 struct __align__(16) Book {
-  using Sp = Split<NQ>;
-  static constexpr int NC = Sp::kC;
-  uint64_t full[Sp::kStages], empty[Sp::kStages];
-  uint64_t s_full[Sp::kS], s_free[Sp::kS], p_full[Sp::kBuf], o_full[Sp::kBuf];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full[kS], s_free[kS], t_full[kS], m_full[kS], o_full[kS], o_free[kS];
+  uint64_t p_full[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t d_full[kDescs], d_empty[kDescs];
-  uint64_t x_full, x_done, drain[2];
+  uint64_t x_full[2], x_done[2], drain[2];
   uint32_t tmem_base;
   int abort_flag;
   Desc desc[kDescs];
   // (arrays that are read four floats at a time start on 16 bytes)
   // scales of a tile: a page's (key scale, value scale relative to the tile's largest, first and
   // last row that are keys), or with sinks among them each key's
-  alignas(16) float4 page[Sp::kStages][8];
-  alignas(16) float2 key[Sp::kStages][128];
-  alignas(16) uint8_t valid[Sp::kStages][128];
-  float vmax[Sp::kStages];              // largest scale of a value in the tile
-  int info[Sp::kStages];                // kMasked: some key is masked, kByKey: scales key by key
+  alignas(16) float4 page[kStages][8];
+  alignas(16) float2 key[kStages][128];
+  alignas(16) uint8_t valid[kStages][128];
+  float vmax[kStages];              // largest scale of a value in the tile
+  int info[kStages];                // kMasked: some key is masked, kByKey: scales key by key
   alignas(16) float q_scale[2][NQ];
-  alignas(16) float red[2][2][4][NC];   // [group][parity][warp][column]
-  alignas(16) float qs[kSoftmaxWarps][NC];       // [warp][column]: scale of the query
-  alignas(16) uint16_t ref[kSoftmaxWarps][NC];   // [warp][column], bf16: -reference of the tile's probabilities
-  alignas(16) uint16_t be[kSoftmaxWarps][NC];    // [warp][column], bf16: factor from it to the run's reference
-  alignas(16) float2 xml[2][NC];        // (m, l) of a group's columns
+  alignas(16) float top[kS][4][NQ];            // [S buffer][warp][column]: largest score, without the query's scale
+  alignas(16) float qs[8][NQ];                 // [exp warp][column]: scale of the query
+  // of a tile's columns, [S buffer][column], bf16: -reference of its probabilities, factor from
+  // that to the run's reference, and the run's reference
+  alignas(16) uint16_t ref[kS][NQ], be[kS][NQ], run[kS][NQ];
+  float o_vmax[kS];                                // and its value scale
+  float x_m[2][2][NQ], x_l[2][8][NQ];      // [run parity]: reference, row sums of the exp warps
   int blk[kProducers][kMaxList], snk[kProducers][kMaxList];   // a producer's lists of its unit
 };
 
 template <int FMT, int D, int NQ>
 struct Lay {
-  using Sp = Split<NQ>;
   static constexpr uint32_t kTile = 128 * D;                       // bytes of a K or V tile
-  static constexpr uint32_t kQ = Sp::kStages * 2 * kTile;          // 2 buffers of hi, lo rows
+  static constexpr uint32_t kQ = kStages * 2 * kTile;          // 2 buffers of hi, lo rows
   static constexpr uint32_t kQBuf = 2 * NQ * D;
   static constexpr uint32_t kP = kQ + 2 * kQBuf;
   static constexpr uint32_t kPRow = 2 * NQ;                        // bytes of a key's row of P: hi, lo
   static constexpr uint32_t kPBuf = 128 * kPRow;
-  // the groups of the same columns hand each other what the others put out, through the P buffers
-  static constexpr uint32_t kX = 2 * (Sp::kC - Sp::kC / Sp::kSlots) * 128 * 4;
-  static constexpr uint32_t kBook = kP + (Sp::kBuf * kPBuf > kX ? Sp::kBuf * kPBuf : kX);
+  static constexpr uint32_t kBook = kP + 2 * kPBuf;
   using Bk = Book<NQ>;
   static constexpr uint32_t kBytes = kBook + sizeof(Bk) + 1024;
   static constexpr int kAcc = 2 * NQ;                              // accumulator columns of a product: hi, lo
-  static constexpr uint32_t kTmemUsed = (Sp::kS + Sp::kBuf) * kAcc;
+  static constexpr uint32_t kTmemUsed = 2 * kS * kAcc + 3 * NQ;    // S^T, O^T, the sum of O^T, two of P's rows
   static constexpr uint32_t kTmem = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
   static_assert(kTmemUsed <= 512, "exceeds tensor memory");
@@ -500,15 +495,33 @@ __device__ __forceinline__ void split_queries(const CacheAttnArgs& a, const Desc
   }
 }
 
+// NQ fp32 columns of tensor memory times a factor each, that of column n from lane n, or zero.
+template <int NQ>
+__device__ __forceinline__ void scale_columns(uint32_t taddr, float f, bool zero) {
+#pragma unroll 1
+  for (int h = 0; h < NQ; h += 16) {
+    uint32_t r[16];
+    if (!zero) {
+      tmem_ld16(taddr + h, r);
+      tmem_ld_wait();
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const float g = __shfl_sync(0xffffffffu, f, h + n);
+      r[n] = zero ? 0u : __float_as_uint(__uint_as_float(r[n]) * g);
+    }
+    tmem_st16(taddr + h, r);
+  }
+  tmem_st_wait();
+}
+
 // ------------------------------------------------------------------ kernel
 template <int FMT, int D, int NQ, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
   using SM = Lay<FMT, D, NQ>;
-  using Sp = Split<NQ>;
-  constexpr int STAGES = Sp::kStages;
-  constexpr int NC = Sp::kC;
+  constexpr int STAGES = kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   auto* bk = reinterpret_cast<Book<NQ>*>(smem + SM::kBook);
@@ -520,24 +533,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk->full[i], 2);                // the copies' bytes, the keys' scales
       mbar_init(&bk->empty[i], 1);
     }
-    for (int i = 0; i < Sp::kS; ++i) {
+    for (int i = 0; i < kS; ++i) {
       mbar_init(&bk->s_full[i], 2);              // the product, and the warp that has seen the tile's scales
-      mbar_init(&bk->s_free[i], 4 * Sp::kPer);
-    }
-    for (int i = 0; i < Sp::kBuf; ++i) {
-      mbar_init(&bk->p_full[i], 4 * Sp::kPer);
-      mbar_init(&bk->o_full[i], 1);
+      mbar_init(&bk->s_free[i], 4);
+      mbar_init(&bk->t_full[i], 4);
+      mbar_init(&bk->m_full[i], 1);
+      mbar_init(&bk->o_full[i], 2);              // the product, and the warp that has seen P's reference
+      mbar_init(&bk->o_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bk->p_full[i], 4);
       mbar_init(&bk->q_full[i], kQParts);
-      mbar_init(&bk->q_empty[i], 1 + kSoftmaxWarps);   // the last QK, and the warps that read the scales
+      mbar_init(&bk->q_empty[i], 1 + 9);         // the last QK, and the warps that read the scales
+      mbar_init(&bk->x_full[i], 8);
+      mbar_init(&bk->x_done[i], 4);
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&bk->d_full[i], 1);
       mbar_init(&bk->d_empty[i], kSoftmaxWarps + 2);   // softmax and MMA warps
     }
-    mbar_init(&bk->x_full, kSoftmaxWarps);
-    mbar_init(&bk->x_done, kSoftmaxWarps);
     mbar_init(&bk->drain[0], 1);
     mbar_init(&bk->drain[1], 1);
     bk->abort_flag = 0;
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t tmem = bk->tmem_base;
-  const uint32_t tS = tmem, tO = tmem + Sp::kS * SM::kAcc;
+  const uint32_t tS = tmem, tO = tS + kS * SM::kAcc, tAcc = tO + kS * SM::kAcc, tSum = tAcc + NQ;
 
   if (warp >= kProducer && warp < kProducer + kProducers) {
     // ------------------------------------------------------------ producers
@@ -962,9 +976,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (const int je = j + n; j < je; ++j) {
         const int s = j % STAGES;
         if (qk) {
-          const int sb = j % Sp::kS;
+          const int sb = j % kS;
           if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
-          if (j >= Sp::kS && !wait(&bk->s_free[sb], (j / Sp::kS - 1) & 1)) break;
+          if (j >= kS && !wait(&bk->s_free[sb], (j / kS - 1) & 1)) break;
           tc_fence_after();
           const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
           const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
@@ -977,8 +991,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&bk->s_full[sb]);
           }
         } else {
-          const int buf = j % Sp::kBuf;
-          if (!wait(&bk->p_full[buf], (j / Sp::kBuf) & 1)) break;
+          const int buf = j & 1, ob = j % kS;
+          if (j >= kS && !wait(&bk->o_free[ob], (j / kS - 1) & 1)) break;
+          if (!wait(&bk->p_full[buf], (j >> 1) & 1)) break;
           if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
           tc_fence_after();
           const uint64_t vd = k0 + static_cast<uint64_t>((s * 2 + 1) * SM::kTile / 16);
@@ -986,9 +1001,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elected) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma8<FMT>(tO + buf * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id, ks > 0 ? 1u : 0u);
-            mma_commit(&bk->o_full[buf]);
+              mma8<FMT>(tO + ob * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id, ks > 0 ? 1u : 0u);
+            mma_commit(&bk->o_full[ob]);
             mma_commit(&bk->empty[s]);
+            mbar_arrive(&bk->o_full[ob]);
           }
         }
         __syncwarp();
@@ -1002,46 +1018,52 @@ __global__ void __launch_bounds__(kThreads, 1)
            !__any_sync(0xffffffffu, globaltimer() - w0 > 500000000ull)) {
     }
   } else {
-    // ------------------------------------------------------------ softmax groups
-    const int grp = warp >> 2, wq = warp & 3;
+    // ------------------------------------------------------------ softmax stages
+    const int wq = warp & 3;
     const int t = threadIdx.x & 127;             // key of the tile == TMEM lane == dim of O^T
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const int slot = grp / Sp::kPer;             // tiles j with j % kSlots == slot
-    const int c0 = grp % Sp::kPer * NC;          // first column
-    const int bar = 1 + grp;
-    const int lc = lane & (NC - 1);              // the column that this lane follows (the same in all warps)
     bool ok = true;
-    int n_x = 0;                                 // exchanges so far
-    int par = 0;
-    // A warp whose wait ran out goes on without waits or tensor memory to the end of the run, where
-    // the whole group leaves: its four warps always take the same barriers.
-    auto wait = [&](uint64_t* bar_, int parity) {
-      if (ok) ok = wait_phase(bar_, parity, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_SOFTMAX);
+    auto wait = [&](uint64_t* bar, int parity) {
+      return ok = wait_phase(bar, parity, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_SOFTMAX);
     };
-    for (int di = 0;; ++di) {
-      const int ds = di % kDescs, qb = di & 1;
-      wait(&bk->d_full[ds], (di / kDescs) & 1);
-      Desc d{};
-      if (ok) d = bk->desc[ds];
+    // the next run; false at the end
+    Desc d;
+    auto next_run = [&](int di) {
+      const int ds = di % kDescs;
+      if (!wait(&bk->d_full[ds], (di / kDescs) & 1)) return false;
+      d = bk->desc[ds];
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&bk->d_empty[ds]);
-      if (ok && d.n > 0) {
-        if (di == 0) {
-          split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 1 + warp, kQParts);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bk->q_full[0]);
-        }
-        wait(&bk->q_full[qb], (di >> 1) & 1);
+      if (lane == 0) mbar_arrive(&bk->d_empty[ds]);
+      if (d.n == 0) return false;
+      if (di == 0) {                             // the first run's query rows: nothing else to do yet
+        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 1 + warp, kQParts);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bk->q_full[0]);
       }
-      if (bar_red_or(bar, 128, !ok) || d.n == 0) break;      // the whole group leaves together
-      // (a zero query or scale: with the smallest normal number instead, every finite score is
-      // still 0, and a masked key's -infinity stays what it is)
-      auto no_zero = [](float v) { return v == 0.f ? 1.17549435e-38f : v; };
-      const float qs = no_zero(bk->q_scale[qb][c0 + lc]);              // of the column this lane follows
-      if (lane < NC) bk->qs[warp][lane] = qs;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
+      return true;
+    };
+    // what the scales of tile stage s say about this thread's key: (scale, factor of its value);
+    // off: it is masked
+    auto key_of = [&](int s, bool& off) {
+      const int info = bk->info[s];
+      const float4 pg = bk->page[s][t >> a.page_shift];
+      float2 key = make_float2(pg.x, pg.y);
+      off = false;
+      if (info != 0) {
+        asm volatile("" ::: "memory");           // (a branch: few tiles come here)
+        if (info & kByKey) {
+          key = bk->key[s][t];
+          off = bk->valid[s][t] == 0;
+        } else {
+          const int r = t & (a.page - 1);
+          off = r < __float_as_int(pg.z) || r >= __float_as_int(pg.w);
+        }
+      }
+      return key;
+    };
+    if (warp < kExpWarp) {
+      // ---------------------------------------------------------- largest scores, references
       // A tile's probabilities are relative to a reference of its own, the next whole number (that
       // bf16 holds) above its largest score in units of log2. (Against a running maximum instead,
       // all that lies 2^-18 below one large key, an attention sink, would be rounded away, and with
@@ -1049,270 +1071,257 @@ __global__ void __launch_bounds__(kThreads, 1)
       // largest is, or 2^-17.) Sums over tiles are relative to m_ref, the reference of the run's
       // first tile with keys, which moves up only when another is above it by 30: fp32 has the
       // range, no sum is rescaled tile by tile, and the factor between the two is an exact power of
-      // two. Whole numbers make both 16 bits wide: handing them from a column's lane to all
-      // threads costs shared-memory bandwidth, of which the tensor cores take half.
-      float2 acc[NC / 2], lsum[NC / 2];
-      uint32_t be2[NC / 2] = {};                 // factors of the group's last tile (pairs of bf16)
-      float be_v = 0.f;                          // and its value scale
-      float m_ref = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NC / 2; ++n) acc[n] = lsum[n] = make_float2(0.f, 0.f);
-      // adds O^T of tile j, in its buffer, to the sums
-      auto collect = [&](int j) {
-        const int buf = j % Sp::kBuf;
-        wait(&bk->o_full[buf], (j / Sp::kBuf) & 1);
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < NC; h += 8) {
-          uint32_t r[8], r2[8];
-          tmem_ld8(tO + buf * SM::kAcc + lane_addr + c0 + h, r);
-          tmem_ld8(tO + buf * SM::kAcc + NQ + lane_addr + c0 + h, r2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float2 o = mul2(both2<FMT>(r + 2 * n, r2 + 2 * n), make_float2(be_v, be_v));
-            acc[h / 2 + n] = fma2(bf16_pair(be2[h / 2 + n]), o, acc[h / 2 + n]);
-          }
+      // two. Whole numbers make all three 16 bits wide: handing them to all threads costs
+      // shared-memory bandwidth, of which the tensor cores take half.
+      const int lc = lane & (NQ - 1);            // the column that this lane follows
+      for (int di = 0; next_run(di); ++di) {
+        float m_ref = -INFINITY, qs = 0.f;
+        if (warp == 0) {
+          // (a zero query or scale: with the smallest normal number instead, every finite score is
+          // still 0, and a masked key's -infinity stays what it is)
+          const int qb = di & 1;
+          if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
+          qs = bk->q_scale[qb][lc];
+          if (qs == 0.f) qs = 1.17549435e-38f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
         }
-        tc_fence_before();
-      };
-      const int jb = d.j0, je = d.j0 + d.n;
-      const int j_first = jb + (slot - jb % Sp::kSlots + Sp::kSlots) % Sp::kSlots;
-      int s = j_first % STAGES;
-      for (int j = j_first; j < je; j += Sp::kSlots) {
-        const int buf = j % Sp::kBuf, sb = j % Sp::kS;
-        wait(&bk->s_full[sb], (j / Sp::kS) & 1);   // (and with it the tile's scales and bytes)
-        const int info = bk->info[s];
-        const float4 pg = bk->page[s][t >> a.page_shift];
-        const float vmax = bk->vmax[s];
-        float2 key = make_float2(pg.x, pg.y);
-        bool off = false;                        // this thread's key is masked
-        if (info != 0) {
-          asm volatile("" ::: "memory");         // (a branch: few tiles come here)
-          if (info & kByKey) {
-            key = bk->key[s][t];
-            off = bk->valid[s][t] == 0;
-          } else {
-            const int r = t & (a.page - 1);
-            off = r < __float_as_int(pg.z) || r >= __float_as_int(pg.w);
-          }
-        }
-        float2 x[NC / 2];
-        if (ok) {
+        for (int j = d.j0; j < d.j0 + d.n; ++j) {
+          const int s = j % STAGES, sb = j % kS;
+          if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;   // (and with it the tile's scales and bytes)
           tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < NC; h += 16) {
+          bool off;
+          const float ks = key_of(s, off).x;
+          const float vmax = bk->vmax[s];
+#pragma unroll 1
+          for (int h = 0; h < NQ; h += 16) {
             uint32_t r[16], r2[16];
-            tmem_ld16(tS + sb * SM::kAcc + lane_addr + c0 + h, r);
-            tmem_ld16(tS + sb * SM::kAcc + NQ + lane_addr + c0 + h, r2);
+            tmem_ld16(tS + sb * SM::kAcc + lane_addr + h, r);
+            tmem_ld16(tS + sb * SM::kAcc + NQ + lane_addr + h, r2);
             tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < 8; ++n) x[h / 2 + n] = mul2(both2<FMT>(r + 2 * n, r2 + 2 * n), make_float2(key.x, key.x));
+            for (int n = 0; n < 16; n += 4) {
+              float2 x0 = mul2(both2<FMT>(r + n, r2 + n), make_float2(ks, ks));
+              float2 x1 = mul2(both2<FMT>(r + n + 2, r2 + n + 2), make_float2(ks, ks));
+              if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
+              float4 m;
+              m.x = warp_max_nan(x0.x);
+              m.y = warp_max_nan(x0.y);
+              m.z = warp_max_nan(x1.x);
+              m.w = warp_max_nan(x1.y);
+              if (lane == 0) *reinterpret_cast<float4*>(&bk->top[sb][wq][h + n]) = m;
+            }
           }
-          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bk->s_free[sb]);
-        } else {
-#pragma unroll
-          for (int n = 0; n < NC / 2; ++n) x[n] = make_float2(0.f, 0.f);
-        }
-        if (info != 0) {
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int n = 0; n < NC / 2; ++n)
-            x[n] = make_float2(off ? -INFINITY : x[n].x, off ? -INFINITY : x[n].y);
-        }
-        // the largest of each column: over the warp, then over the group's four warps; lane n of
-        // every warp follows column n
-        par ^= 1;
-#pragma unroll
-        for (int n = 0; n < NC; n += 4) {
-          float4 m;
-          m.x = warp_max_nan(x[n / 2].x);
-          m.y = warp_max_nan(x[n / 2].y);
-          m.z = warp_max_nan(x[n / 2 + 1].x);
-          m.w = warp_max_nan(x[n / 2 + 1].y);
-          if (lane == 0) *reinterpret_cast<float4*>(&bk->red[grp][par][wq][n]) = m;
-        }
-        // The buffers of P and O^T are free once the product that used them has been added, which
-        // was under way while this tile's scores were formed
-        if (j - Sp::kBuf >= jb) collect(j - Sp::kBuf);
-        named_bar_sync(bar, 128);
-        float ref = 0.f, fe;
-        {
-          const float* rl = &bk->red[grp][par][0][0];
-          const float mt = max3_nan(max_nan(rl[lc], rl[NC + lc]), rl[2 * NC + lc], rl[3 * NC + lc]);
+          if (lane == 0) mbar_arrive(&bk->t_full[sb]);
+          if (warp != 0) continue;
+          if (!wait(&bk->t_full[sb], (j / kS) & 1)) break;
+          const float* tp = &bk->top[sb][0][lc];
+          const float mt = max3_nan(max_nan(tp[0], tp[NQ]), tp[2 * NQ], tp[3 * NQ]);
           uint32_t r16 = 0;                      // bf16 of the reference
-          float al = 1.f;
-          fe = 0.f;
+          uint32_t be16 = 0;                     // and of the factor
           if (mt != -INFINITY) {                 // (a tile without keys adds nothing)
             const uint32_t c = __float_as_uint(ceilf(mt * qs));
             r16 = mt != mt ? 0x7fc0u : (c & 0x80000000u) ? c >> 16 : (c + 0xffffu) >> 16;
-            ref = __uint_as_float(r16 << 16);
-            if (ref > m_ref + 30.f || m_ref == -INFINITY) {
-              al = exp2_approx(m_ref - ref);
-              m_ref = ref;
-            }
-            fe = exp2_approx(ref - m_ref);
+            const float ref = __uint_as_float(r16 << 16);
+            if (ref > m_ref + 30.f || m_ref == -INFINITY) m_ref = ref;
+            const float e = ref - m_ref;         // a whole number
+            be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
           }
-          if (lane < NC) {
-            bk->ref[warp][lane] = static_cast<uint16_t>(r16 ^ 0x8000u);
-            bk->be[warp][lane] = static_cast<uint16_t>(__float_as_uint(fe) >> 16);
-          }
-          if (__any_sync(0xffffffffu, al != 1.f)) {                    // the same in the group's four warps
-#pragma unroll
-            for (int n = 0; n < NC / 2; ++n) {
-              const float2 f = make_float2(__shfl_sync(0xffffffffu, al, 2 * n), __shfl_sync(0xffffffffu, al, 2 * n + 1));
-              lsum[n] = mul2(lsum[n], f);
-              acc[n] = mul2(acc[n], f);
-            }
-          }
+          // the entries are free once the sum warps are done with the last tile there
+          if (j >= kS && !wait(&bk->o_free[sb], (j / kS - 1) & 1)) break;
+          bk->ref[sb][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
+          bk->be[sb][lc] = static_cast<uint16_t>(be16);
+          bk->run[sb][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
+          if (lane == 0) bk->o_vmax[sb] = vmax;
           __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->m_full[sb]);
         }
-        // P is written as it is held, a key to a row, hi then lo: an MN-major operand. (Stored
-        // query-major, a byte at a time, the stores alone took 1500 cycles of a tile.)
-        uint8_t* pbuf = smem + SM::kP + buf * SM::kPBuf;
-#pragma unroll
-        for (int h = 0; h < NC; h += 16) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = h + 4 * i;
-            const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[warp][n]);
-            const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[warp][n]);
-            const float2 v0 = fma2(x[n / 2], make_float2(qv.x, qv.y), bf16_pair(rv.x));
-            const float2 v1 = fma2(x[n / 2 + 1], make_float2(qv.z, qv.w), bf16_pair(rv.y));
-            x[n / 2] = make_float2(exp2_approx(v0.x), exp2_approx(v0.y));
-            x[n / 2 + 1] = make_float2(exp2_approx(v1.x), exp2_approx(v1.y));
-            split4<FMT>(mul2(x[n / 2], make_float2(key.y, key.y)), mul2(x[n / 2 + 1], make_float2(key.y, key.y)), hi[i], lo[i]);
+        if (!ok) break;
+      }
+    } else if (warp < kSumWarp) {
+      // ---------------------------------------------------------- probabilities
+      const int we = warp - kExpWarp, grp = we >> 2;   // the group takes the tiles j with j % 2 == grp
+      const int lc = lane & (NQ - 1);
+      for (int di = 0; next_run(di); ++di) {
+        const int qb = di & 1;
+        if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
+        {
+          const float qs = bk->q_scale[qb][lc];
+          bk->qs[we][lc] = qs == 0.f ? 1.17549435e-38f : qs;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
+        float m_ref = -INFINITY;                 // of the lane's column, what the row sums are relative to
+        const uint32_t tl = tSum + grp * NQ + lane_addr;
+        scale_columns<NQ>(tl, 0.f, true);
+        const int je = d.j0 + d.n;
+        for (int j = d.j0 + ((d.j0 ^ grp) & 1); j < je; j += 2) {
+          const int s = j % STAGES, sb = j % kS;
+          if (!wait(&bk->m_full[sb], (j / kS) & 1)) break;
+          if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;
+          tc_fence_after();
+          bool off;
+          const float2 key = key_of(s, off);
+          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[sb][lc]) << 16);
+          if (__any_sync(0xffffffffu, m_new != m_ref)) {               // (the run's first tile, seldom another)
+            scale_columns<NQ>(tl, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
+            m_ref = m_new;
           }
-          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (c0 + h) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (NQ + c0 + h) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        // A masked key's values may be anything, NaN codes included, and 0 * NaN is NaN
-        if (FMT == FOCUS_CACHE_E4M3 && off && c0 == 0) {
-          uint8_t* v = smem + (s * 2 + 1) * SM::kTile;
+          // the buffer of P is free once the product that used it is done
+          if (j >= 2 && !wait(&bk->o_full[(j - 2) % kS], ((j - 2) / kS) & 1)) break;
+          // P is written as it is held, a key to a row, hi then lo: an MN-major operand. (Stored
+          // query-major, a byte at a time, the stores alone took 1500 cycles of a tile.)
+          uint8_t* pbuf = smem + SM::kP + (j & 1) * SM::kPBuf;
+          const uint32_t ts = tS + sb * SM::kAcc + lane_addr;
+#pragma unroll 1
+          for (int h = 0; h < NQ; h += 16) {
+            uint32_t r[16], r2[16], rl[16];
+            tmem_ld16(ts + h, r);
+            tmem_ld16(ts + NQ + h, r2);
+            tmem_ld16(tl + h, rl);
+            tmem_ld_wait();
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + row_chunk<D>(t, c)) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bk->p_full[buf]);
-        // while the product is under way: the tile's row sums, and its factors for O^T
-        be_v = vmax;
+            for (int i = 0; i < 4; ++i) {
+              float2 x0 = mul2(both2<FMT>(r + 4 * i, r2 + 4 * i), make_float2(key.x, key.x));
+              float2 x1 = mul2(both2<FMT>(r + 4 * i + 2, r2 + 4 * i + 2), make_float2(key.x, key.x));
+              if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
+              const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[sb][h + 4 * i]);
+              const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[sb][h + 4 * i]);
+              const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[we][h + 4 * i]);
+              float2 p0 = fma2(x0, make_float2(qv.x, qv.y), bf16_pair(rv.x));
+              float2 p1 = fma2(x1, make_float2(qv.z, qv.w), bf16_pair(rv.y));
+              p0 = make_float2(exp2_approx(p0.x), exp2_approx(p0.y));
+              p1 = make_float2(exp2_approx(p1.x), exp2_approx(p1.y));
+              const float2 l0 = fma2(p0, bf16_pair(bv.x), make_float2(__uint_as_float(rl[4 * i]), __uint_as_float(rl[4 * i + 1])));
+              const float2 l1 = fma2(p1, bf16_pair(bv.y), make_float2(__uint_as_float(rl[4 * i + 2]), __uint_as_float(rl[4 * i + 3])));
+              rl[4 * i] = __float_as_uint(l0.x);
+              rl[4 * i + 1] = __float_as_uint(l0.y);
+              rl[4 * i + 2] = __float_as_uint(l1.x);
+              rl[4 * i + 3] = __float_as_uint(l1.y);
+              split4<FMT>(mul2(p0, make_float2(key.y, key.y)), mul2(p1, make_float2(key.y, key.y)), hi[i], lo[i]);
+            }
+            tmem_st16(tl + h, rl);
+            *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, h / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(pbuf + row_chunk<SM::kPRow>(t, (NQ + h) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          tmem_st_wait();
+          // A masked key's values may be anything, NaN codes included, and 0 * NaN is NaN
+          if (FMT == FOCUS_CACHE_E4M3 && off) {
+            uint8_t* v = smem + (s * 2 + 1) * SM::kTile;
 #pragma unroll
-        for (int h = 0; h < NC / 8; ++h) {
-          const uint4 w = reinterpret_cast<const uint4*>(bk->be[warp])[h];
-          be2[4 * h] = w.x;
-          be2[4 * h + 1] = w.y;
-          be2[4 * h + 2] = w.z;
-          be2[4 * h + 3] = w.w;
-        }
-#pragma unroll
-        for (int n = 0; n < NC / 2; ++n) lsum[n] = fma2(x[n], bf16_pair(be2[n]), lsum[n]);
-        __syncwarp();
-        s += Sp::kSlots;
-        if (s >= STAGES) s -= STAGES;
-      }
-      // the product still under way
-      if (j_first < je) collect(je - 1 - (je - 1 - j_first) % Sp::kSlots);
-      // row sums over the 128 keys
-      float l;
-      {
-        float ls[NC];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) ls[n] = n & 1 ? lsum[n / 2].y : lsum[n / 2].x;
-        if constexpr (NC == 32) {
-          warp_sum_scatter<32>(ls);              // column n in lane n
-          l = ls[0];
-        } else {
-          warp_sum_scatter16(ls);                // column n in lane 2 n
-          l = __shfl_sync(0xffffffffu, ls[0], (2 * lane) & 31);
-        }
-        par ^= 1;
-        if (lane < NC) bk->red[grp][par][wq][lane] = l;
-        if (bar_red_or(bar, 128, !ok)) break;
-        const float* rd = &bk->red[grp][par][0][0];
-        l = (rd[lc] + rd[NC + lc]) + (rd[2 * NC + lc] + rd[3 * NC + lc]);
-      }
-      // Groups of the same columns: each puts out a part of them and gets the others' sums for
-      // these through the P buffers, which no product reads any more once all groups have
-      // collected theirs.
-      auto sum_of = [&](int n) { return n & 1 ? acc[n / 2].y : acc[n / 2].x; };
-      constexpr int OC = NC / Sp::kSlots;        // columns that a group puts out
-      const int n0 = slot * OC;
-      float out[OC];
-      if constexpr (Sp::kSlots > 1) {
-        if (lane == 0) mbar_arrive(&bk->x_full);
-        wait(&bk->x_full, 0);
-        if (bar_red_or(bar, 128, !ok)) break;
-        float* xch = reinterpret_cast<float*>(smem + SM::kP);        // [group of the sums][other's rank][OC][128]
-#pragma unroll
-        for (int o = 0; o < Sp::kSlots; ++o) {
-          if (o == slot) continue;
-          // group (o, c0) reads this group's sums of its columns as its source number (slot - o - 1)
-          const int to = o * Sp::kPer + grp % Sp::kPer, rank = (slot - o - 1 + Sp::kSlots) % Sp::kSlots;
-#pragma unroll
-          for (int i = 0; i < OC; ++i) xch[((to * (Sp::kSlots - 1) + rank) * OC + i) * 128 + t] = sum_of(o * OC + i);
-        }
-        if (wq == 0 && lane < NC) bk->xml[grp][lane] = make_float2(m_ref, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bk->x_full);
-        wait(&bk->x_full, 1);
-        if (bar_red_or(bar, 128, !ok)) break;
-        float M = m_ref;
-        float2 om[Sp::kSlots - 1];
-#pragma unroll
-        for (int r = 0; r < Sp::kSlots - 1; ++r) {
-          om[r] = bk->xml[(slot + 1 + r) % Sp::kSlots * Sp::kPer + grp % Sp::kPer][lc];
-          M = max_nan(M, om[r].x);
-        }
-        const float f0 = l == 0.f ? 0.f : exp2_approx(m_ref - M);
-        l *= f0;
-#pragma unroll
-        for (int i = 0; i < OC; ++i) {
-          float mine = sum_of(i);
-#pragma unroll
-          for (int o = 1; o < Sp::kSlots; ++o) mine = slot == o ? sum_of(o * OC + i) : mine;
-          out[i] = __shfl_sync(0xffffffffu, f0, n0 + i) * mine;
-        }
-#pragma unroll
-        for (int r = 0; r < Sp::kSlots - 1; ++r) {
-          const float f = om[r].y == 0.f ? 0.f : exp2_approx(om[r].x - M);
-          l += f * om[r].y;
-#pragma unroll
-          for (int i = 0; i < OC; ++i)
-            out[i] += __shfl_sync(0xffffffffu, f, n0 + i) * xch[((grp * (Sp::kSlots - 1) + r) * OC + i) * 128 + t];
-        }
-        m_ref = M;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bk->x_done);
-        wait(&bk->x_done, n_x & 1);
-        ++n_x;
-      } else {
-#pragma unroll
-        for (int i = 0; i < OC; ++i) out[i] = sum_of(i);
-      }
-      // out: columns c0 + n0 .. of the slice
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int i = 0; i < OC; ++i) {
-        const int n = c0 + n0 + i;
-        const float f = __shfl_sync(0xffffffffu, inv, n0 + i);
-        if (n < d.rows && t < D) {
-          if (d.slot >= 0) {
-            a.part_o[(static_cast<size_t>(d.slot) * NQ + n) * D + t] = out[i];
-          } else {
-            const int r = d.row0 + n, qh = r / a.qcap, qi = r - qh * a.qcap;
-            const size_t row = (static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi;
-            a.O[row * D + t] = __float2bfloat16_rn(qi < d.nq ? out[i] * f : 0.f);
+            for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + row_chunk<D>(t, c)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bk->p_full[j & 1]);
+            mbar_arrive(&bk->s_free[sb]);
           }
         }
+        if (!ok) break;
+        // row sums over the warp's keys, for the sum warps, which have the run before last behind them
+        if (di >= 2 && !wait(&bk->x_done[qb], ((di >> 1) - 1) & 1)) break;
+#pragma unroll 1
+        for (int h = 0; h < NQ; h += 16) {
+          uint32_t rl[16];
+          tmem_ld16(tl + h, rl);
+          tmem_ld_wait();
+          float ls[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) ls[n] = __uint_as_float(rl[n]);
+          warp_sum_scatter16(ls);                // column h + n in lanes 2 n and 2 n + 1
+          bk->x_l[qb][we][h + (lane >> 1)] = ls[0];
+        }
+        if (wq == 0) bk->x_m[qb][grp][lc] = m_ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bk->x_full[qb]);
       }
-      if (d.slot >= 0 && wq == 0 && lane >= n0 && lane < n0 + OC && c0 + lane < d.rows)
-        a.part_ml[static_cast<size_t>(d.slot) * NQ + c0 + lane] = make_float2(m_ref, l);
+    } else {
+      // ---------------------------------------------------------- sums and output
+      const int ws = warp - kSumWarp;
+      const int lc = lane & (NQ - 1);            // the column that this lane follows
+      for (int di = 0; next_run(di); ++di) {
+        const int qb = di & 1;
+        float m_ref = -INFINITY;
+        const uint32_t ta = tAcc + lane_addr;
+        scale_columns<NQ>(ta, 0.f, true);
+        for (int j = d.j0; j < d.j0 + d.n; ++j) {
+          const int ob = j % kS;
+          if (!wait(&bk->o_full[ob], (j / kS) & 1)) break;
+          tc_fence_after();
+          const float2 vmax = make_float2(bk->o_vmax[ob], bk->o_vmax[ob]);
+          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[ob][lc]) << 16);
+          if (__any_sync(0xffffffffu, m_new != m_ref)) {
+            scale_columns<NQ>(ta, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
+            m_ref = m_new;
+          }
+#pragma unroll 1
+          for (int h = 0; h < NQ; h += 16) {
+            uint32_t r[16], r2[16], ra[16];
+            tmem_ld16(tO + ob * SM::kAcc + lane_addr + h, r);
+            tmem_ld16(tO + ob * SM::kAcc + NQ + lane_addr + h, r2);
+            tmem_ld16(ta + h, ra);
+            uint32_t w[8];
+            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(&bk->be[ob][h]);
+            *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(&bk->be[ob][h + 8]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float2 v = fma2(mul2(bf16_pair(w[n]), vmax), both2<FMT>(r + 2 * n, r2 + 2 * n),
+                                    make_float2(__uint_as_float(ra[2 * n]), __uint_as_float(ra[2 * n + 1])));
+              ra[2 * n] = __float_as_uint(v.x);
+              ra[2 * n + 1] = __float_as_uint(v.y);
+            }
+            tmem_st16(ta + h, ra);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->o_free[ob]);
+        }
+        if (!ok) break;
+        // join: the exp groups' row sums, each relative to its own reference, and O
+        if (!wait(&bk->x_full[qb], (di >> 1) & 1)) break;
+        const float m0 = bk->x_m[qb][0][lc], m1 = bk->x_m[qb][1][lc];
+        const float M = max3_nan(m_ref, m0, m1);
+        const float* xl = &bk->x_l[qb][0][lc];
+        const float l0 = (xl[0] + xl[NQ]) + (xl[2 * NQ] + xl[3 * NQ]), l1 = (xl[4 * NQ] + xl[5 * NQ]) + (xl[6 * NQ] + xl[7 * NQ]);
+        const float l = (l0 == 0.f ? 0.f : l0 * exp2_approx(m0 - M)) + (l1 == 0.f ? 0.f : l1 * exp2_approx(m1 - M));
+        float fo = m_ref == -INFINITY ? 0.f : exp2_approx(m_ref - M);
+        if (d.slot < 0) fo *= l == 0.f ? 0.f : 1.f / l;
+        if (d.slot >= 0 && ws == 0 && lane < NQ && lane < d.rows)
+          a.part_ml[static_cast<size_t>(d.slot) * NQ + lane] = make_float2(M, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bk->x_done[qb]);
+        // output: every thread its dim of every row
+        int qh = d.row0 / a.qcap, qi = d.row0 - qh * a.qcap;
+#pragma unroll 1
+        for (int h = 0; h < NQ && h < d.rows; h += 16) {
+          uint32_t ra[16];
+          tmem_ld16(ta + h, ra);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int n = h + i;
+            const float v = __uint_as_float(ra[i]) * __shfl_sync(0xffffffffu, fo, n);
+            if (n < d.rows && t < D) {
+              if (d.slot >= 0) {
+                a.part_o[(static_cast<size_t>(d.slot) * NQ + n) * D + t] = v;
+              } else {
+                const size_t row = (static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi;
+                a.O[row * D + t] = __float2bfloat16_rn(qi < d.nq ? v : 0.f);
+              }
+            }
+            if (++qi == a.qcap) {
+              qi = 0;
+              ++qh;
+            }
+          }
+        }
+      }
     }
     if (!ok) bk->abort_flag = 1;
   }
@@ -1431,9 +1440,10 @@ int page_map(CUtensorMap* map, const void* base, const focus_cache* c) {
   return FOCUS_OK;
 }
 
-// Query rows a CTA works on: 16 for single tokens of grouped heads, 32 for a step's active rows,
-// 64 where a KV head has more (each slice reads the codes again, from L2).
-int rows_per_cta(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Query rows a CTA works on: 16 for single tokens of grouped heads, 32 for a step's active rows;
+// where a KV head has more, every slice of 32 reads the codes again, from L2. (Slices of 64 need
+// 64 sums a thread beside 96 registers, and the exp warps take as long for 64 rows as for twice 32.)
+int rows_per_cta(int rows) { return rows <= 16 ? 16 : 32; }
 
 template <int FMT, int D, int NQ, bool SPARSE>
 int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnArgs& a, cudaStream_t stream) {
@@ -1457,11 +1467,8 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAt
 
 template <int FMT, int D, bool SPARSE>
 int launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnArgs& a, cudaStream_t stream) {
-  switch (rows_per_cta(a.g * a.qcap)) {
-    case 16: return launch_attention<FMT, D, 16, SPARSE>(mk, mv, a, stream);
-    case 32: return launch_attention<FMT, D, 32, SPARSE>(mk, mv, a, stream);
-    default: return launch_attention<FMT, D, 64, SPARSE>(mk, mv, a, stream);
-  }
+  return rows_per_cta(a.g * a.qcap) == 16 ? launch_attention<FMT, D, 16, SPARSE>(mk, mv, a, stream)
+                                          : launch_attention<FMT, D, 32, SPARSE>(mk, mv, a, stream);
 }
 
 template <bool SPARSE>
