@@ -33,13 +33,16 @@
 // tiles or more are under way and the latencies of the hand-overs (mbarriers, tensor memory,
 // shuffles: half of a tile's way) are covered by the other tiles:
 //   16, 17  producers, a tile each in turn (TMA for pages, cp.async for sink rows)
-//   18      issues S^T = K Q^T (and prepares the query rows, and owns tensor memory)
-//   0-3     the largest score of every column in each warp's 32 keys, and warp 0 the references
+//   18      issues S^T = K Q^T, and sets the references (and owns tensor memory)
+//   0-3     the largest score of every column in each warp's 32 keys (and the query rows)
 //   4-11    two groups, a tile each in turn: exp, row sums, hi and lo of P
 //   19      issues O^T = V^T P^T
 //   12-15   sum of O^T over tiles; at the end of a unit, the output
 // With one group taking a tile from its scores to its sum, and two such groups, a tile took 2200
-// cycles, most of them latency; the memory brings one every 1370.
+// cycles, most of them latency; the memory brings one every 1370. The loops over columns stay
+// short (16 columns, rolled, with what lasts from tile to tile in tensor memory instead of
+// registers): the stages run side by side on every scheduler, and unrolled over 32 columns their
+// code, together, left the instruction cache (3.2 of 13 warp cycles per instruction waited for one).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -56,7 +59,7 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kProducers = 2;
 constexpr int kProducer = kSoftmaxWarps, kMmaS = kProducer + kProducers, kMmaO = kMmaS + 1;
 constexpr int kThreads = (kMmaO + 1) * 32;
-constexpr int kQParts = kSoftmaxWarps + 1;   // warps that prepare the first queries
+constexpr int kQParts = kSoftmaxWarps;   // warps that prepare the first queries
 constexpr int kMaxList = 1024;          // sinks, kept blocks
 constexpr int kDescs = 4;
 constexpr int kMasked = 1, kByKey = 2;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bk->p_full[i], 4);
       mbar_init(&bk->q_full[i], kQParts);
-      mbar_init(&bk->q_empty[i], 1 + 9);         // the last QK, and the warps that read the scales
+      mbar_init(&bk->q_empty[i], 2 + 8);         // the last QK, and the warps that read the scales
       mbar_init(&bk->x_full[i], 8);
       mbar_init(&bk->x_done[i], 4);
     }
@@ -954,47 +957,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, int parity) {
       return ok = wait_phase(bar, parity, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_MMA);
     };
+    auto test = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    const int lc = lane & (NQ - 1);              // the column whose reference this lane sets
     int j = 0;
     for (int di = 0; ok; ++di) {
       const int ds = di % kDescs, qb = di & 1;
       if (!wait(&bk->d_full[ds], (di / kDescs) & 1)) break;
-      const Desc d = bk->desc[ds];
-      const int n = d.n;
+      const int n = bk->desc[ds].n, je = j + n;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk->d_empty[ds]);
       if (n == 0) break;
-      if (qk) {
-        // the run's query rows: the first run's shared with the softmax warps, which have nothing
-        // else to do yet, later ones' ahead of those warps by the buffers of S^T
-        if (di >= 2 && !wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1)) break;
-        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], 0, di == 0 ? kQParts : 1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_n(&bk->q_full[qb], di == 0 ? 1 : kQParts);
-        if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
-      }
-      for (const int je = j + n; j < je; ++j) {
-        const int s = j % STAGES;
-        if (qk) {
-          const int sb = j % kS;
-          if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
-          if (j >= kS && !wait(&bk->s_free[sb], (j / kS - 1) & 1)) break;
-          tc_fence_after();
-          const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
-          const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
-          if (elected) {
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-              mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id, ks > 0 ? 1u : 0u);
-            mma_commit(&bk->s_full[sb]);
-            if (j == je - 1) mma_commit(&bk->q_empty[qb]);
-            mbar_arrive(&bk->s_full[sb]);
-          }
-        } else {
-          const int buf = j & 1, ob = j % kS;
+      if (!qk) {
+        for (; j < je; ++j) {
+          const int s = j % kStages, buf = j & 1, ob = j % kS;
           if (j >= kS && !wait(&bk->o_free[ob], (j / kS - 1) & 1)) break;
           if (!wait(&bk->p_full[buf], (j >> 1) & 1)) break;
-          if (!wait(&bk->full[s], (j / STAGES) & 1)) break;
+          if (!wait(&bk->full[s], (j / kStages) & 1)) break;
           tc_fence_after();
           const uint64_t vd = k0 + static_cast<uint64_t>((s * 2 + 1) * SM::kTile / 16);
           const uint64_t pd = p0 + static_cast<uint64_t>(buf * SM::kPBuf / 16);
@@ -1006,8 +984,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&bk->empty[s]);
             mbar_arrive(&bk->o_full[ob]);
           }
+          __syncwarp();
         }
-        __syncwarp();
+        continue;
+      }
+      if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
+      // (a zero query or scale: with the smallest normal number instead, every finite score is
+      // still 0, and a masked key's -infinity stays what it is)
+      float qs = bk->q_scale[qb][lc], m_ref = -INFINITY;
+      if (qs == 0.f) qs = 1.17549435e-38f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
+      // whichever can go on next: the product of tile j, or the references of tile jr
+      unsigned long long idle = 0;               // since when neither could
+      for (int jr = j; jr < je;) {
+        bool did = false;
+        const int rb = jr % kS;
+        if (jr < j && test(&bk->t_full[rb], (jr / kS) & 1) && (jr < kS || test(&bk->o_free[rb], (jr / kS - 1) & 1))) {
+          // A tile's probabilities are relative to a reference of its own, the next whole number
+          // (that bf16 holds) above its largest score in units of log2. (Against a running maximum
+          // instead, all that lies 2^-18 below one large key, an attention sink, would be rounded
+          // away, and with thousands of such keys a part of the result; so, no more than
+          // 128 * 2^-18 of a tile's own largest is, or 2^-17.) Sums over tiles are relative to
+          // m_ref, the reference of the run's first tile with keys, which moves up only when another
+          // is above it by 30: fp32 has the range, no sum is rescaled tile by tile, and the factor
+          // between the two is an exact power of two. Whole numbers make all three 16 bits wide:
+          // handing them to all threads costs shared-memory bandwidth, of which the tensor cores
+          // take half.
+          const float* tp = &bk->top[rb][0][lc];
+          const float mt = max3_nan(max_nan(tp[0], tp[NQ]), tp[2 * NQ], tp[3 * NQ]);
+          uint32_t r16 = 0;                      // bf16 of the reference
+          uint32_t be16 = 0;                     // and of the factor
+          if (mt != -INFINITY) {                 // (a tile without keys adds nothing)
+            const uint32_t c = __float_as_uint(ceilf(mt * qs));
+            r16 = mt != mt ? 0x7fc0u : (c & 0x80000000u) ? c >> 16 : (c + 0xffffu) >> 16;
+            const float ref = __uint_as_float(r16 << 16);
+            if (ref > m_ref + 30.f || m_ref == -INFINITY) m_ref = ref;
+            const float e = ref - m_ref;         // a whole number
+            be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
+          }
+          bk->ref[rb][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
+          bk->be[rb][lc] = static_cast<uint16_t>(be16);
+          bk->run[rb][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
+          if (lane == 0) bk->o_vmax[rb] = bk->vmax[jr % kStages];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bk->m_full[rb]);
+          ++jr;
+          did = true;
+        }
+        const int s = j % kStages, sb = j % kS;
+        if (j < je && j - jr < kS && test(&bk->full[s], (j / kStages) & 1) &&
+            (j < kS || test(&bk->s_free[sb], (j / kS - 1) & 1))) {
+          tc_fence_after();
+          const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
+          const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
+          if (elected) {
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks)
+              mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id, ks > 0 ? 1u : 0u);
+            mma_commit(&bk->s_full[sb]);
+            if (j == je - 1) mma_commit(&bk->q_empty[qb]);
+            mbar_arrive(&bk->s_full[sb]);
+          }
+          __syncwarp();
+          ++j;
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+          continue;
+        }
+        const unsigned long long now = globaltimer();
+        if (idle == 0) idle = now;
+        bool stop = *abort_flag != 0;
+        if (now - idle > kWaitLimitNs) {
+          *abort_flag = 1;
+          if (lane == 0) record_dev_error(a.dev_err, DEV_ERR_TIMEOUT_MMA);
+          stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop)) {
+          ok = false;
+          break;
+        }
       }
     }
     // (after a wait that ran out, products may still be under way)
@@ -1036,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bk->d_empty[ds]);
       if (d.n == 0) return false;
       if (di == 0) {                             // the first run's query rows: nothing else to do yet
-        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], 1 + warp, kQParts);
+        split_queries<FMT, D, NQ>(a, d, smem + SM::kQ, bk->q_scale[0], warp, kQParts);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bk->q_full[0]);
@@ -1063,28 +1121,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       return key;
     };
     if (warp < kExpWarp) {
-      // ---------------------------------------------------------- largest scores, references
-      // A tile's probabilities are relative to a reference of its own, the next whole number (that
-      // bf16 holds) above its largest score in units of log2. (Against a running maximum instead,
-      // all that lies 2^-18 below one large key, an attention sink, would be rounded away, and with
-      // thousands of such keys a part of the result; so, no more than 128 * 2^-18 of a tile's own
-      // largest is, or 2^-17.) Sums over tiles are relative to m_ref, the reference of the run's
-      // first tile with keys, which moves up only when another is above it by 30: fp32 has the
-      // range, no sum is rescaled tile by tile, and the factor between the two is an exact power of
-      // two. Whole numbers make all three 16 bits wide: handing them to all threads costs
-      // shared-memory bandwidth, of which the tensor cores take half.
-      const int lc = lane & (NQ - 1);            // the column that this lane follows
+      // ---------------------------------------------------------- largest scores
       for (int di = 0; next_run(di); ++di) {
-        float m_ref = -INFINITY, qs = 0.f;
-        if (warp == 0) {
-          // (a zero query or scale: with the smallest normal number instead, every finite score is
-          // still 0, and a masked key's -infinity stays what it is)
+        if (di > 0) {
+          // the run's query rows, while the later stages are still at the last run's tiles
           const int qb = di & 1;
-          if (!wait(&bk->q_full[qb], (di >> 1) & 1)) break;
-          qs = bk->q_scale[qb][lc];
-          if (qs == 0.f) qs = 1.17549435e-38f;
+          if (di >= 2 && !wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1)) break;
+          split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], warp, 4);
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bk->q_empty[qb]);
+          if (lane == 0) mbar_arrive_n(&bk->q_full[qb], kQParts / 4);
         }
         for (int j = d.j0; j < d.j0 + d.n; ++j) {
           const int s = j % STAGES, sb = j % kS;
@@ -1092,7 +1138,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           bool off;
           const float ks = key_of(s, off).x;
-          const float vmax = bk->vmax[s];
 #pragma unroll 1
           for (int h = 0; h < NQ; h += 16) {
             uint32_t r[16], r2[16];
@@ -1114,28 +1159,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bk->t_full[sb]);
-          if (warp != 0) continue;
-          if (!wait(&bk->t_full[sb], (j / kS) & 1)) break;
-          const float* tp = &bk->top[sb][0][lc];
-          const float mt = max3_nan(max_nan(tp[0], tp[NQ]), tp[2 * NQ], tp[3 * NQ]);
-          uint32_t r16 = 0;                      // bf16 of the reference
-          uint32_t be16 = 0;                     // and of the factor
-          if (mt != -INFINITY) {                 // (a tile without keys adds nothing)
-            const uint32_t c = __float_as_uint(ceilf(mt * qs));
-            r16 = mt != mt ? 0x7fc0u : (c & 0x80000000u) ? c >> 16 : (c + 0xffffu) >> 16;
-            const float ref = __uint_as_float(r16 << 16);
-            if (ref > m_ref + 30.f || m_ref == -INFINITY) m_ref = ref;
-            const float e = ref - m_ref;         // a whole number
-            be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
-          }
-          // the entries are free once the sum warps are done with the last tile there
-          if (j >= kS && !wait(&bk->o_free[sb], (j / kS - 1) & 1)) break;
-          bk->ref[sb][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
-          bk->be[sb][lc] = static_cast<uint16_t>(be16);
-          bk->run[sb][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
-          if (lane == 0) bk->o_vmax[sb] = vmax;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bk->m_full[sb]);
         }
         if (!ok) break;
       }
