@@ -157,12 +157,16 @@ struct Desc {               // a run of tiles of one unit that this CTA works on
 };
 
 constexpr int kStages = 5;              // tiles in the K/V ring
-constexpr int kS = 3;                   // buffers of S^T, and of O^T
+constexpr int kS = 4, kO = 2;           // buffers of S^T, of O^T
+// Entries for what the later stages need to know of a tile. Tile j's may be overwritten by tile
+// j + kE's without a wait: its score product waited for P of tile j + kE - kS, that for the
+// product of P of tile j + kE - kS - 2, and that for the sums of tile j + kE - kS - 2 - kO.
+constexpr int kE = kS + 2 + kO;
 
 template <int NQ>
 struct __align__(16) Book {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full[kS], s_free[kS], t_full[kS], m_full[kS], o_full[kS], o_free[kS];
+  uint64_t s_full[kS], s_free[kS], t_full[kS], m_full[kS], o_full[kO], o_free[kO];
   uint64_t p_full[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t d_full[kDescs], d_empty[kDescs];
@@ -181,10 +185,10 @@ struct __align__(16) Book {
   alignas(16) float q_scale[2][NQ];
   alignas(16) float top[kS][4][NQ];            // [S buffer][warp][column]: largest score, without the query's scale
   alignas(16) float qs[8][NQ];                 // [exp warp][column]: scale of the query
-  // of a tile's columns, [S buffer][column], bf16: -reference of its probabilities, factor from
-  // that to the run's reference, and the run's reference
-  alignas(16) uint16_t ref[kS][NQ], be[kS][NQ], run[kS][NQ];
-  float o_vmax[kS];                                // and its value scale
+  // of a tile's columns, [entry][column], bf16: -reference of its probabilities, factor from that
+  // to the run's reference, and the run's reference
+  alignas(16) uint16_t ref[kE][NQ], be[kE][NQ], run[kE][NQ];
+  float o_vmax[kE];                                // and its value scale
   float x_m[2][2][NQ], x_l[2][8][NQ];      // [run parity]: reference, row sums of the exp warps
   int blk[kProducers][kMaxList], snk[kProducers][kMaxList];   // a producer's lists of its unit
 };
@@ -201,7 +205,7 @@ struct Lay {
   using Bk = Book<NQ>;
   static constexpr uint32_t kBytes = kBook + sizeof(Bk) + 1024;
   static constexpr int kAcc = 2 * NQ;                              // accumulator columns of a product: hi, lo
-  static constexpr uint32_t kTmemUsed = 2 * kS * kAcc + 3 * NQ;    // S^T, O^T, the sum of O^T, two of P's rows
+  static constexpr uint32_t kTmemUsed = (kS + kO) * kAcc + 3 * NQ;    // S^T, O^T, the sum of O^T, two of P's rows
   static constexpr uint32_t kTmem = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
   static_assert(kTmemUsed <= 512, "exceeds tensor memory");
@@ -541,7 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk->s_free[i], 4);
       mbar_init(&bk->t_full[i], 4);
       mbar_init(&bk->m_full[i], 1);
-      mbar_init(&bk->o_full[i], 2);              // the product, and the warp that has seen P's reference
+    }
+    for (int i = 0; i < kO; ++i) {
+      mbar_init(&bk->o_full[i], 2);              // the product, and the warp that has seen P's entry
       mbar_init(&bk->o_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t tmem = bk->tmem_base;
-  const uint32_t tS = tmem, tO = tS + kS * SM::kAcc, tAcc = tO + kS * SM::kAcc, tSum = tAcc + NQ;
+  const uint32_t tS = tmem, tO = tS + kS * SM::kAcc, tAcc = tO + kO * SM::kAcc, tSum = tAcc + NQ;
 
   if (warp >= kProducer && warp < kProducer + kProducers) {
     // ------------------------------------------------------------ producers
@@ -969,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n == 0) break;
       if (!qk) {
         for (; j < je; ++j) {
-          const int s = j % kStages, buf = j & 1, ob = j % kS;
-          if (j >= kS && !wait(&bk->o_free[ob], (j / kS - 1) & 1)) break;
+          const int s = j % kStages, buf = j & 1, ob = j % kO;
+          if (j >= kO && !wait(&bk->o_free[ob], (j / kO - 1) & 1)) break;
           if (!wait(&bk->p_full[buf], (j >> 1) & 1)) break;
           if (!wait(&bk->full[s], (j / kStages) & 1)) break;
           tc_fence_after();
@@ -1000,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int jr = j; jr < je;) {
         bool did = false;
         const int rb = jr % kS;
-        if (jr < j && test(&bk->t_full[rb], (jr / kS) & 1) && (jr < kS || test(&bk->o_free[rb], (jr / kS - 1) & 1))) {
+        if (jr < j && test(&bk->t_full[rb], (jr / kS) & 1)) {
           // A tile's probabilities are relative to a reference of its own, the next whole number
           // (that bf16 holds) above its largest score in units of log2. (Against a running maximum
           // instead, all that lies 2^-18 below one large key, an attention sink, would be rounded
@@ -1023,10 +1029,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float e = ref - m_ref;         // a whole number
             be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
           }
-          bk->ref[rb][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
-          bk->be[rb][lc] = static_cast<uint16_t>(be16);
-          bk->run[rb][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
-          if (lane == 0) bk->o_vmax[rb] = bk->vmax[jr % kStages];
+          const int e = jr % kE;
+          bk->ref[e][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
+          bk->be[e][lc] = static_cast<uint16_t>(be16);
+          bk->run[e][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
+          if (lane == 0) bk->o_vmax[e] = bk->vmax[jr % kStages];
           __syncwarp();
           if (lane == 0) mbar_arrive(&bk->m_full[rb]);
           ++jr;
@@ -1180,19 +1187,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         scale_columns<NQ>(tl, 0.f, true);
         const int je = d.j0 + d.n;
         for (int j = d.j0 + ((d.j0 ^ grp) & 1); j < je; j += 2) {
-          const int s = j % STAGES, sb = j % kS;
+          const int s = j % STAGES, sb = j % kS, e = j % kE;
           if (!wait(&bk->m_full[sb], (j / kS) & 1)) break;
           if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;
           tc_fence_after();
           bool off;
           const float2 key = key_of(s, off);
-          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[sb][lc]) << 16);
+          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[e][lc]) << 16);
           if (__any_sync(0xffffffffu, m_new != m_ref)) {               // (the run's first tile, seldom another)
             scale_columns<NQ>(tl, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
             m_ref = m_new;
           }
           // the buffer of P is free once the product that used it is done
-          if (j >= 2 && !wait(&bk->o_full[(j - 2) % kS], ((j - 2) / kS) & 1)) break;
+          if (j >= 2 && !wait(&bk->o_full[(j - 2) % kO], ((j - 2) / kO) & 1)) break;
           // P is written as it is held, a key to a row, hi then lo: an MN-major operand. (Stored
           // query-major, a byte at a time, the stores alone took 1500 cycles of a tile.)
           uint8_t* pbuf = smem + SM::kP + (j & 1) * SM::kPBuf;
@@ -1204,14 +1211,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16(ts + NQ + h, r2);
             tmem_ld16(tl + h, rl);
             tmem_ld_wait();
+            if (h == NQ - 16) {                  // the scores have been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bk->s_free[sb]);
+            }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float2 x0 = mul2(both2<FMT>(r + 4 * i, r2 + 4 * i), make_float2(key.x, key.x));
               float2 x1 = mul2(both2<FMT>(r + 4 * i + 2, r2 + 4 * i + 2), make_float2(key.x, key.x));
               if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
-              const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[sb][h + 4 * i]);
-              const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[sb][h + 4 * i]);
+              const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[e][h + 4 * i]);
+              const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[e][h + 4 * i]);
               const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[we][h + 4 * i]);
               float2 p0 = fma2(x0, make_float2(qv.x, qv.y), bf16_pair(rv.x));
               float2 p1 = fma2(x1, make_float2(qv.z, qv.w), bf16_pair(rv.y));
@@ -1239,10 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bk->p_full[j & 1]);
-            mbar_arrive(&bk->s_free[sb]);
-          }
+          if (lane == 0) mbar_arrive(&bk->p_full[j & 1]);
         }
         if (!ok) break;
         // row sums over the warp's keys, for the sum warps, which have the run before last behind them
@@ -1272,11 +1281,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ta = tAcc + lane_addr;
         scale_columns<NQ>(ta, 0.f, true);
         for (int j = d.j0; j < d.j0 + d.n; ++j) {
-          const int ob = j % kS;
-          if (!wait(&bk->o_full[ob], (j / kS) & 1)) break;
+          const int ob = j % kO, e = j % kE;
+          if (!wait(&bk->o_full[ob], (j / kO) & 1)) break;
           tc_fence_after();
-          const float2 vmax = make_float2(bk->o_vmax[ob], bk->o_vmax[ob]);
-          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[ob][lc]) << 16);
+          const float2 vmax = make_float2(bk->o_vmax[e], bk->o_vmax[e]);
+          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[e][lc]) << 16);
           if (__any_sync(0xffffffffu, m_new != m_ref)) {
             scale_columns<NQ>(ta, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
             m_ref = m_new;
@@ -1288,8 +1297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16(tO + ob * SM::kAcc + NQ + lane_addr + h, r2);
             tmem_ld16(ta + h, ra);
             uint32_t w[8];
-            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(&bk->be[ob][h]);
-            *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(&bk->be[ob][h + 8]);
+            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(&bk->be[e][h]);
+            *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(&bk->be[e][h + 8]);
             tmem_ld_wait();
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
