@@ -101,15 +101,15 @@ __device__ __forceinline__ Sequence sequence_of(const CacheAttnArgs& a, int b) {
   Sequence s{};
   const int top = a.table_cols * a.page;
   if (SPARSE) {
-    const int g0 = a.g0[b];
+    const int g0 = __ldcg(a.g0 + b);
     s.gs = max(0, min(g0, top));
     s.ge = static_cast<int>(max(0LL, min(static_cast<long long>(g0) + a.G, static_cast<long long>(top))));
-    s.P = max(0, min(a.P[b], s.gs));
+    s.P = max(0, min(__ldcg(a.P + b), s.gs));
     s.n_gen = s.ge > s.gs ? ((s.ge - 1) >> a.page_shift) - (s.gs >> a.page_shift) + 1 : 0;
     s.n_pages = s.n_gen + a.C;
     s.tiles = (s.n_pages * a.page + a.S + 127) >> 7;
   } else {
-    s.len = max(0, min(a.lens[b], top));
+    s.len = max(0, min(__ldcg(a.lens + b), top));
     s.n_pages = (s.len + a.page - 1) >> a.page_shift;
     s.tiles = (s.len + 127) >> 7;
   }
@@ -139,13 +139,18 @@ __device__ __forceinline__ int length_before(const CacheAttnArgs& a, int b) {
   return n;
 }
 
-// Share i of `shares` contiguous shares of an axis of length T begins at i * T / shares.
+// Share i of `shares` contiguous shares of an axis of length T begins at i * T / shares (without
+// a 64-bit division, which is a few hundred cycles at the head of every call).
 __device__ __forceinline__ int share_begin(int i, int T, int shares) {
-  return static_cast<int>(static_cast<long long>(i) * T / shares);
+  const unsigned n = static_cast<unsigned>(shares), whole = static_cast<unsigned>(T) / n;
+  return static_cast<int>(i * whole + i * (T - whole * n) / n);
 }
 // The share that place x falls in.
 __device__ __forceinline__ int share_of(int x, int T, int shares) {
-  return static_cast<int>((static_cast<long long>(x + 1) * shares - 1) / T);
+  int s = min(shares - 1, static_cast<int>(__fdividef(static_cast<float>(x) * shares, static_cast<float>(T))));
+  while (s > 0 && share_begin(s, T, shares) > x) --s;
+  while (s + 1 < shares && share_begin(s + 1, T, shares) <= x) ++s;
+  return s;
 }
 
 // ------------------------------------------------------------------ shared memory
@@ -438,9 +443,8 @@ __device__ __forceinline__ void split_queries(const CacheAttnArgs& a, const Desc
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       const int q = q0 + step * i, r = d.row0 + q;
-      const int qh = r / a.qcap, qi = r - qh * a.qcap;
-      const bool real = q < d.rows && qi < d.nq;
-      const __nv_bfloat16* src = a.Q + ((static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi) * D + lane * E;
+      const bool real = q < d.rows && (d.nq == a.qcap || r % a.qcap < d.nq);
+      const __nv_bfloat16* src = a.Q + ((static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g) * a.qcap + r) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         uint32_t w = 0u;
@@ -575,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();                   // (after the wait, so that what follows may read the inputs at once)
   const uint32_t tmem = bk->tmem_base;
   const uint32_t tS = tmem, tO = tS + kS * SM::kAcc, tAcc = tO + kO * SM::kAcc, tSum = tAcc + NQ;
 
@@ -1328,28 +1332,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.part_ml[static_cast<size_t>(d.slot) * NQ + lane] = make_float2(M, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bk->x_done[qb]);
-        // output: every thread its dim of every row
-        int qh = d.row0 / a.qcap, qi = d.row0 - qh * a.qcap;
+        // output: every thread its dim of every row, row after row in memory
+        const unsigned none = __ballot_sync(0xffffffffu, d.nq < a.qcap && (d.row0 + lc) % a.qcap >= d.nq);
+        float* part = a.part_o + static_cast<size_t>(max(d.slot, 0)) * NQ * D + t;
+        __nv_bfloat16* out = a.O + ((static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g) * a.qcap + d.row0) * D + t;
 #pragma unroll 1
-        for (int h = 0; h < NQ && h < d.rows; h += 16) {
-          uint32_t ra[16];
-          tmem_ld16(ta + h, ra);
+        for (int h = 0; h < d.rows; h += 8) {
+          uint32_t ra[8];
+          tmem_ld8(ta + h, ra);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int n = h + i;
             const float v = __uint_as_float(ra[i]) * __shfl_sync(0xffffffffu, fo, n);
             if (n < d.rows && t < D) {
-              if (d.slot >= 0) {
-                a.part_o[(static_cast<size_t>(d.slot) * NQ + n) * D + t] = v;
-              } else {
-                const size_t row = (static_cast<size_t>(d.b) * a.Hq + d.kvh * a.g + qh) * a.qcap + qi;
-                a.O[row * D + t] = __float2bfloat16_rn(qi < d.nq ? v : 0.f);
-              }
-            }
-            if (++qi == a.qcap) {
-              qi = 0;
-              ++qh;
+              if (d.slot >= 0) part[n * D] = v;
+              else out[n * D] = __float2bfloat16_rn((none >> n) & 1u ? 0.f : v);
             }
           }
         }
@@ -1365,69 +1363,76 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the units that several CTAs worked on (a warp per query row, a lane holds
 // D / 32 dims): weights 2^(m - M) over the parts' (m, l), 32 parts at a time. Units without
-// keys get zeros; units of one CTA are done already.
+// keys get zeros; units of one CTA are done already. Which parts there are follows from the
+// inputs alone, so it is worked out before the attention is done: two warps of 64 registers find
+// room beside an attention CTA. (All wait for it, those without work too: what follows in the
+// stream waits for this kernel only.)
+constexpr int kJoinWarps = 2;
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnArgs a, int NQ) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 16) cache_combine_kernel(const CacheAttnArgs a, int NQ) {
   constexpr int E = D / 32;
   griddep_launch_dependents();
-  griddep_wait();
   const int lane = lane_id();
-  const int rows = a.g * a.qcap;                            // of a KV head
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + warp_id();
-  if (w >= static_cast<long long>(a.B) * a.Hkv * rows) return;
-  const int bh = static_cast<int>(w / rows), r = static_cast<int>(w - static_cast<long long>(bh) * rows);
-  const int b = bh / a.Hkv, kvh = bh - b * a.Hkv, slice = r / a.slice_rows, n = r - slice * a.slice_rows;
-  const Sequence q = sequence_of<SPARSE>(a, b);
-  const int heads = a.Hkv * a.n_slices;
-  const int qh = r / a.qcap, qi = r - qh * a.qcap;
-  __nv_bfloat16* O = a.O + ((static_cast<size_t>(b) * a.Hq + kvh * a.g + qh) * a.qcap + qi) * D + lane * E;
-  const int nq = a.n_q ? max(0, min(a.n_q[b], a.qcap)) : a.qcap;
+  const unsigned rows = static_cast<unsigned>(a.g * a.qcap);   // of a KV head
+  const unsigned w = blockIdx.x * kJoinWarps + warp_id();
+  const unsigned bh = w / rows, r = w - bh * rows;
+  const int b = static_cast<int>(bh) / a.Hkv, kvh = static_cast<int>(bh) - b * a.Hkv;
+  if (b >= a.B) {
+    griddep_wait();
+    return;
+  }
+  const int slice = static_cast<int>(r) / a.slice_rows, n = static_cast<int>(r) - slice * a.slice_rows;
+  const int tiles = sequence_of<SPARSE>(a, b).tiles;
+  const int qi = static_cast<int>(r) % a.qcap;
+  const bool real = !a.n_q || qi < __ldcg(a.n_q + b);
+  int s0 = 0, s1 = -1;
+  if (tiles > 0) {
+    const int heads = a.Hkv * a.n_slices;
+    const int T = length_of_all<SPARSE>(a) * heads;
+    const int shares = min(a.grid, T);
+    const int x0 = length_before<SPARSE>(a, b) * heads + (kvh * a.n_slices + slice) * unit_length(tiles) + kLead;
+    s0 = share_of(x0, T, shares), s1 = share_of(x0 + tiles - 1, T, shares);
+  }
+  griddep_wait();
+  if (s0 == s1) return;
   float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  float l = 0.f;
-  if (q.tiles > 0) {
-    const int T = length_of_all<SPARSE>(a) * heads;
-    const int shares = min(a.grid, T);
-    const int x0 = length_before<SPARSE>(a, b) * heads + (kvh * a.n_slices + slice) * unit_length(q.tiles) + kLead;
-    const int s0 = share_of(x0, T, shares), s1 = share_of(x0 + q.tiles - 1, T, shares);
-    if (s0 == s1) return;
-    float M = -INFINITY;
-    for (int c0 = s0; c0 <= s1; c0 += 32) {
-      const int c = c0 + lane;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (c <= s1) ml = a.part_ml[(static_cast<size_t>(2 * c) + (c == s0 ? 1 : 0)) * NQ + n];
-      const float mn = max_nan(M, warp_max_nan(ml.x));
-      const float back = l == 0.f ? 0.f : exp2_approx(M - mn);
-      const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - mn);
-      float lw = f * ml.y;
+  float l = 0.f, M = -INFINITY;
+  for (int c0 = s0; c0 <= s1; c0 += 32) {
+    const int c = c0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (c <= s1) ml = a.part_ml[static_cast<size_t>(2 * c + (c == s0 ? 1 : 0)) * NQ + n];
+    const float mn = max_nan(M, warp_max_nan(ml.x));
+    const float back = l == 0.f ? 0.f : exp2_approx(M - mn);
+    const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - mn);
+    float lw = f * ml.y;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
-      l = l * back + lw;
-      M = mn;
+    for (int off = 16; off; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+    l = l * back + lw;
+    M = mn;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= back;
-      const int cn = min(32, s1 - c0 + 1);
+    for (int e = 0; e < E; ++e) o[e] *= back;
+    const int cn = min(32, s1 - c0 + 1);
 #pragma unroll 8
-      for (int i = 0; i < cn; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* src = a.part_o + ((static_cast<size_t>(2 * (c0 + i)) + (c0 + i == s0 ? 1 : 0)) * NQ + n) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          o[0] += fi * v.x;
-          o[1] += fi * v.y;
-          o[2] += fi * v.z;
-          o[3] += fi * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          o[0] += fi * v.x;
-          o[1] += fi * v.y;
-        }
+    for (int i = 0; i < cn; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* src = a.part_o + (static_cast<size_t>(2 * (c0 + i) + (c0 + i == s0 ? 1 : 0)) * NQ + n) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[0] += fi * v.x;
+        o[1] += fi * v.y;
+        o[2] += fi * v.z;
+        o[3] += fi * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[0] += fi * v.x;
+        o[1] += fi * v.y;
       }
     }
   }
-  const float inv = (qi < nq && l != 0.f) ? 1.f / l : 0.f;
-  const bool real = qi < nq;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  __nv_bfloat16* O = a.O + (static_cast<size_t>(bh) * rows + r) * D + lane * E;
   uint32_t pk[E / 2];
 #pragma unroll
   for (int e = 0; e < E; e += 2) pk[e / 2] = real ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
@@ -1486,7 +1491,8 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAt
   note_launch();
   if (e == cudaSuccess) {
     const long long rows = static_cast<long long>(a.B) * a.Hkv * a.g * a.qcap;
-    e = launch_k(cache_combine_kernel<D, SPARSE>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, a, NQ);
+    e = launch_k(cache_combine_kernel<D, SPARSE>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
+                 dim3(kJoinWarps * 32), 0, stream, a, NQ);
     note_launch();
   }
   if (e != cudaSuccess) {
@@ -1513,7 +1519,7 @@ int run_cache_attention(CacheAttnArgs a, const focus_cache* c, void* ws, cudaStr
   const long long per_unit = SPARSE ? (static_cast<long long>((a.G + a.page - 2) / a.page + 1 + a.C) * a.page + a.S + 127) / 128
                                     : (static_cast<long long>(a.table_cols) * a.page + 127) / 128;
   const long long most = static_cast<long long>(a.B) * a.Hkv * a.n_slices * (per_unit + kLead);
-  if (most >= (1LL << 31) || static_cast<long long>(a.B) * a.Hkv * rows >= (1LL << 32)) {
+  if (most >= (1LL << 31) || static_cast<long long>(a.B) * a.Hkv * rows >= (1LL << 31)) {
     set_error("cache attention: %lld tiles of 128 keys in one call", most);
     return FOCUS_ERR_UNSUPPORTED;
   }
