@@ -96,20 +96,27 @@ struct Sequence {
   int len;              // dense
 };
 
-template <bool SPARSE>
+// EARLY: before the wait for the kernels in front, past L1, which may hold what an earlier kernel read.
+template <bool EARLY>
+__device__ __forceinline__ int word(const int32_t* p) {
+  if constexpr (EARLY) return __ldcg(p);
+  else return *p;
+}
+
+template <bool SPARSE, bool EARLY = false>
 __device__ __forceinline__ Sequence sequence_of(const CacheAttnArgs& a, int b) {
   Sequence s{};
   const int top = a.table_cols * a.page;
   if (SPARSE) {
-    const int g0 = __ldcg(a.g0 + b);
+    const int g0 = word<EARLY>(a.g0 + b);
     s.gs = max(0, min(g0, top));
     s.ge = static_cast<int>(max(0LL, min(static_cast<long long>(g0) + a.G, static_cast<long long>(top))));
-    s.P = max(0, min(__ldcg(a.P + b), s.gs));
+    s.P = max(0, min(word<EARLY>(a.P + b), s.gs));
     s.n_gen = s.ge > s.gs ? ((s.ge - 1) >> a.page_shift) - (s.gs >> a.page_shift) + 1 : 0;
     s.n_pages = s.n_gen + a.C;
     s.tiles = (s.n_pages * a.page + a.S + 127) >> 7;
   } else {
-    s.len = max(0, min(__ldcg(a.lens + b), top));
+    s.len = max(0, min(word<EARLY>(a.lens + b), top));
     s.n_pages = (s.len + a.page - 1) >> a.page_shift;
     s.tiles = (s.len + 127) >> 7;
   }
@@ -124,18 +131,18 @@ __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffff
 __device__ __forceinline__ int unit_length(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
 
 // Length of the axis for one head slice of all sequences (a warp; the same in every lane).
-template <bool SPARSE>
+template <bool SPARSE, bool EARLY = false>
 __device__ __forceinline__ int length_of_all(const CacheAttnArgs& a) {
   int n = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) n += warp_sum(b0 + lane_id() < a.B ? unit_length(sequence_of<SPARSE>(a, b0 + lane_id()).tiles) : 0);
+  for (int b0 = 0; b0 < a.B; b0 += 32) n += warp_sum(b0 + lane_id() < a.B ? unit_length(sequence_of<SPARSE, EARLY>(a, b0 + lane_id()).tiles) : 0);
   return n;
 }
 
 // The part of it before sequence b.
-template <bool SPARSE>
+template <bool SPARSE, bool EARLY>
 __device__ __forceinline__ int length_before(const CacheAttnArgs& a, int b) {
   int n = 0;
-  for (int b0 = 0; b0 < b; b0 += 32) n += warp_sum(b0 + lane_id() < b ? unit_length(sequence_of<SPARSE>(a, b0 + lane_id()).tiles) : 0);
+  for (int b0 = 0; b0 < b; b0 += 32) n += warp_sum(b0 + lane_id() < b ? unit_length(sequence_of<SPARSE, EARLY>(a, b0 + lane_id()).tiles) : 0);
   return n;
 }
 
@@ -161,7 +168,9 @@ struct Desc {               // a run of tiles of one unit that this CTA works on
   int slot;                 // where the partial result goes, -1 = straight into O
 };
 
-constexpr int kStages = 5;              // tiles in the K/V ring
+// Tiles in the rings of K and of V. A key tile is free once its scores are out, a value tile only
+// after the way through the probabilities, so that takes more of them.
+constexpr int kK = 4, kV = 6;
 constexpr int kS = 4, kO = 2;           // buffers of S^T, of O^T
 // Entries for what the later stages need to know of a tile. Tile j's may be overwritten by tile
 // j + kE's without a wait: its score product waited for P of tile j + kE - kS, that for the
@@ -170,7 +179,7 @@ constexpr int kE = kS + 2 + kO;
 
 template <int NQ>
 struct __align__(16) Book {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
   uint64_t s_full[kS], s_free[kS], t_full[kS], m_full[kS], o_full[kO], o_free[kO];
   uint64_t p_full[2];
   uint64_t q_full[2], q_empty[2];
@@ -182,11 +191,11 @@ struct __align__(16) Book {
   // (arrays that are read four floats at a time start on 16 bytes)
   // scales of a tile: a page's (key scale, value scale relative to the tile's largest, first and
   // last row that are keys), or with sinks among them each key's
-  alignas(16) float4 page[kStages][8];
-  alignas(16) float2 key[kStages][128];
-  alignas(16) uint8_t valid[kStages][128];
-  float vmax[kStages];              // largest scale of a value in the tile
-  int info[kStages];                // kMasked: some key is masked, kByKey: scales key by key
+  alignas(16) float4 page[kV][8];
+  alignas(16) float2 key[kV][128];
+  alignas(16) uint8_t valid[kV][128];
+  float vmax[kV];              // largest scale of a value in the tile
+  int info[kV];                // kMasked: some key is masked, kByKey: scales key by key
   alignas(16) float q_scale[2][NQ];
   alignas(16) float top[kS][4][NQ];            // [S buffer][warp][column]: largest score, without the query's scale
   alignas(16) float qs[8][NQ];                 // [exp warp][column]: scale of the query
@@ -201,7 +210,8 @@ struct __align__(16) Book {
 template <int FMT, int D, int NQ>
 struct Lay {
   static constexpr uint32_t kTile = 128 * D;                       // bytes of a K or V tile
-  static constexpr uint32_t kQ = kStages * 2 * kTile;          // 2 buffers of hi, lo rows
+  static constexpr uint32_t kVRing = kK * kTile;
+  static constexpr uint32_t kQ = kVRing + kV * kTile;              // 2 buffers of hi, lo rows
   static constexpr uint32_t kQBuf = 2 * NQ * D;
   static constexpr uint32_t kP = kQ + 2 * kQBuf;
   static constexpr uint32_t kPRow = 2 * NQ;                        // bytes of a key's row of P: hi, lo
@@ -532,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnArgs a) {
   using SM = Lay<FMT, D, NQ>;
-  constexpr int STAGES = kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   auto* bk = reinterpret_cast<Book<NQ>*>(smem + SM::kBook);
@@ -540,9 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id();
 
   if (warp == kProducer && lane == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&bk->full[i], 2);                // the copies' bytes, the keys' scales
-      mbar_init(&bk->empty[i], 1);
+    for (int i = 0; i < kK; ++i) {
+      mbar_init(&bk->k_full[i], 2);              // the copies' bytes, the tile's scales (and sink rows)
+      mbar_init(&bk->k_empty[i], 1);
+    }
+    for (int i = 0; i < kV; ++i) {
+      mbar_init(&bk->v_full[i], 1);              // the copies' bytes
+      mbar_init(&bk->v_empty[i], 1);
     }
     for (int i = 0; i < kS; ++i) {
       mbar_init(&bk->s_full[i], 2);              // the product, and the warp that has seen the tile's scales
@@ -772,31 +785,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             // way, of as many as find a free stage (afterwards scales go with each tile, or they
             // would hold up its use)
             do {
-              const int j = j0 + tile, s = j % STAGES;
-              if (j >= STAGES) {
-                const uint32_t ph = ((j / STAGES) - 1) & 1;
-                bool got;
-                if (tile == done) {
-                  got = ok = wait_phase(&bk->empty[s], ph, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_PRODUCER);
-                } else {
-                  got = __all_sync(0xffffffffu, mbar_test(&bk->empty[s], ph));
-                }
-                if (!got) break;
-              }
+              const int j = j0 + tile, sk = j % kK, sv = j % kV;
+              auto free_stage = [&](uint64_t* bar, int round) {
+                if (round == 0) return true;
+                if (tile == done)
+                  return ok = wait_phase(bar, (round - 1) & 1, abort_flag, a.dev_err, DEV_ERR_TIMEOUT_PRODUCER);
+                return __all_sync(0xffffffffu, mbar_test(bar, (round - 1) & 1)) != 0;
+              };
+              if (!free_stage(&bk->k_empty[sk], j / kK) || !free_stage(&bk->v_empty[sv], j / kV)) break;
               const int rel = bbase + lane - (tile << tp);           // this lane's page of the tile
               const bool mine = rel >= 0 && rel < ppt && cur.pg >= 0;
               const unsigned any = __ballot_sync(0xffffffffu, mine);
-              if (lane == 0) mbar_arrive_expect_tx(&bk->full[s], static_cast<uint32_t>(__popc(any) * 2 * a.page * D));
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&bk->k_full[sk], static_cast<uint32_t>(__popc(any) * a.page * D));
+                mbar_arrive_expect_tx(&bk->v_full[sv], static_cast<uint32_t>(__popc(any) * a.page * D));
+              }
               __syncwarp();
               if (mine) {
-                const uint32_t dst = smem_u32(smem) + s * 2 * SM::kTile + rel * a.page * D;
+                const uint32_t at = smem_u32(smem) + rel * a.page * D;
+                const uint32_t dk = at + sk * SM::kTile, dv = at + SM::kVRing + sv * SM::kTile;
                 const int z = static_cast<int>(static_cast<long long>(cur.pg) * a.Hkv + kvh);
                 if (once) {
-                  tma_load_3d_hint(dst, &tmK, &bk->full[s], 0, 0, z, policy);
-                  tma_load_3d_hint(dst + SM::kTile, &tmV, &bk->full[s], 0, 0, z, policy);
+                  tma_load_3d_hint(dk, &tmK, &bk->k_full[sk], 0, 0, z, policy);
+                  tma_load_3d_hint(dv, &tmV, &bk->v_full[sv], 0, 0, z, policy);
                 } else {
-                  tma_load_3d(dst, &tmK, &bk->full[s], 0, 0, z);
-                  tma_load_3d(dst + SM::kTile, &tmV, &bk->full[s], 0, 0, z);
+                  tma_load_3d(dk, &tmK, &bk->k_full[sk], 0, 0, z);
+                  tma_load_3d(dv, &tmV, &bk->v_full[sv], 0, 0, z);
                 }
               }
               __syncwarp();
@@ -808,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cold = false;
             finished = true;
             for (; done < tile; done += kProducers) {
-              const int s = (j0 + done) % STAGES;
+              const int s = (j0 + done) % kV, sk = (j0 + done) % kK;
               if (!SPARSE || done * 128 + 128 <= (q.n_pages << a.page_shift)) {
                 // whole pages: each lane its own, and each softmax thread looks up its key's
                 const int rel = bbase + lane - (done << tp);
@@ -819,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   bk->info[s] = (cur.part >> lane) & ((1u << ppt) - 1u) ? kMasked : 0;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bk->full[s]);
+                if (lane == 0) mbar_arrive(&bk->k_full[sk]);
                 if (!resolved && b_end < last) {
                   resolve(nxt);
                   resolved = true;
@@ -894,11 +908,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   ks[e] = __ldg(a.scale[0] + ph);
                   vs[e] = __ldg(a.scale[1] + ph);
                   const long long off = (ph * a.page + (pos & (a.page - 1))) * D;
-                  const uint32_t dst = smem_u32(smem) + s * 2 * SM::kTile;
+                  const uint32_t dk = smem_u32(smem) + sk * SM::kTile, dv = smem_u32(smem) + SM::kVRing + s * SM::kTile;
 #pragma unroll
                   for (int c = 0; c < D / 16; ++c) {
-                    cp_async16(dst + row_chunk<D>(4 * lane + e, c), a.code[0] + off + c * 16, 16);
-                    cp_async16(dst + SM::kTile + row_chunk<D>(4 * lane + e, c), a.code[1] + off + c * 16, 16);
+                    cp_async16(dk + row_chunk<D>(4 * lane + e, c), a.code[0] + off + c * 16, 16);
+                    cp_async16(dv + row_chunk<D>(4 * lane + e, c), a.code[1] + off + c * 16, 16);
                   }
                 }
                 cp_async_wait_all();
@@ -922,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bk->info[s] = kMasked | kByKey;
               }
               __syncwarp();
-              if (lane == 0) mbar_arrive(&bk->full[s]);
+              if (lane == 0) mbar_arrive(&bk->k_full[sk]);
               if (!resolved && b_end < last) {
                 resolve(nxt);
                 resolved = true;
@@ -942,12 +956,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       // a wait ran out: the copies under way still have to land before the CTA may leave
-      for (int j = issued - 1; j >= 0 && j >= issued - STAGES; j -= kProducers) {
+      auto land = [&](uint64_t* bar, int parity) {
         const unsigned long long w0 = globaltimer();
-        if (lane == 0) mbar_arrive(&bk->full[j % STAGES]);
-        while (!__all_sync(0xffffffffu, mbar_test(&bk->full[j % STAGES], (j / STAGES) & 1)) &&
+        while (!__all_sync(0xffffffffu, mbar_test(bar, parity & 1)) &&
                !__any_sync(0xffffffffu, globaltimer() - w0 > 500000000ull)) {
         }
+      };
+      for (int j = issued - 1; j >= 0 && j >= issued - kV; j -= kProducers) {
+        land(&bk->v_full[j % kV], j / kV);
+        if (j < issued - kK) continue;
+        if (lane == 0) mbar_arrive(&bk->k_full[j % kK]);
+        land(&bk->k_full[j % kK], j / kK);
       }
     }
     __syncwarp();
@@ -960,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t elected = elect_one();
     const bool qk = warp == kMmaS;
     const uint32_t id = idesc8<FMT>(2 * NQ, !qk);
-    const uint64_t k0 = tile_desc<D>(smem_u32(smem));
+    const uint64_t k0 = tile_desc<D>(smem_u32(smem)), v0 = tile_desc<D>(smem_u32(smem) + SM::kVRing);
     const uint64_t q0 = tile_desc<D>(smem_u32(smem) + SM::kQ);
     const uint64_t p0 = tile_desc<SM::kPRow>(smem_u32(smem) + SM::kP);
     bool ok = true;
@@ -979,19 +998,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n == 0) break;
       if (!qk) {
         for (; j < je; ++j) {
-          const int s = j % kStages, buf = j & 1, ob = j % kO;
+          const int s = j % kV, buf = j & 1, ob = j % kO;
           if (j >= kO && !wait(&bk->o_free[ob], (j / kO - 1) & 1)) break;
           if (!wait(&bk->p_full[buf], (j >> 1) & 1)) break;
-          if (!wait(&bk->full[s], (j / kStages) & 1)) break;
+          if (!wait(&bk->v_full[s], (j / kV) & 1)) break;
           tc_fence_after();
-          const uint64_t vd = k0 + static_cast<uint64_t>((s * 2 + 1) * SM::kTile / 16);
+          const uint64_t vd = v0 + static_cast<uint64_t>(s * SM::kTile / 16);
           const uint64_t pd = p0 + static_cast<uint64_t>(buf * SM::kPBuf / 16);
           if (elected) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma8<FMT>(tO + ob * SM::kAcc, vd + ks * (32 * D / 16), pd + ks * (32 * SM::kPRow / 16), id, ks > 0 ? 1u : 0u);
             mma_commit(&bk->o_full[ob]);
-            mma_commit(&bk->empty[s]);
+            mma_commit(&bk->v_empty[s]);
             mbar_arrive(&bk->o_full[ob]);
           }
           __syncwarp();
@@ -1037,23 +1056,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           bk->ref[e][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
           bk->be[e][lc] = static_cast<uint16_t>(be16);
           bk->run[e][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
-          if (lane == 0) bk->o_vmax[e] = bk->vmax[jr % kStages];
+          if (lane == 0) bk->o_vmax[e] = bk->vmax[jr % kV];
           __syncwarp();
           if (lane == 0) mbar_arrive(&bk->m_full[rb]);
           ++jr;
           did = true;
         }
-        const int s = j % kStages, sb = j % kS;
-        if (j < je && j - jr < kS && test(&bk->full[s], (j / kStages) & 1) &&
+        const int s = j % kK, sb = j % kS;
+        if (j < je && j - jr < kS && test(&bk->k_full[s], (j / kK) & 1) &&
             (j < kS || test(&bk->s_free[sb], (j / kS - 1) & 1))) {
           tc_fence_after();
-          const uint64_t kd = k0 + static_cast<uint64_t>(s * 2 * SM::kTile / 16);
+          const uint64_t kd = k0 + static_cast<uint64_t>(s * SM::kTile / 16);
           const uint64_t qd = q0 + static_cast<uint64_t>(qb * SM::kQBuf / 16);
           if (elected) {
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks)
               mma8<FMT>(tS + sb * SM::kAcc, kd + ks * 2, qd + ks * 2, id, ks > 0 ? 1u : 0u);
             mma_commit(&bk->s_full[sb]);
+            mma_commit(&bk->k_empty[s]);
             if (j == je - 1) mma_commit(&bk->q_empty[qb]);
             mbar_arrive(&bk->s_full[sb]);
           }
@@ -1144,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_n(&bk->q_full[qb], kQParts / 4);
         }
         for (int j = d.j0; j < d.j0 + d.n; ++j) {
-          const int s = j % STAGES, sb = j % kS;
+          const int s = j % kV, sb = j % kS;
           if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;   // (and with it the tile's scales and bytes)
           tc_fence_after();
           bool off;
@@ -1191,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         scale_columns<NQ>(tl, 0.f, true);
         const int je = d.j0 + d.n;
         for (int j = d.j0 + ((d.j0 ^ grp) & 1); j < je; j += 2) {
-          const int s = j % STAGES, sb = j % kS, e = j % kE;
+          const int s = j % kV, sb = j % kS, e = j % kE;
           if (!wait(&bk->m_full[sb], (j / kS) & 1)) break;
           if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;
           tc_fence_after();
@@ -1247,10 +1267,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st_wait();
           // A masked key's values may be anything, NaN codes included, and 0 * NaN is NaN
-          if (FMT == FOCUS_CACHE_E4M3 && off) {
-            uint8_t* v = smem + (s * 2 + 1) * SM::kTile;
+          if (FMT == FOCUS_CACHE_E4M3 && __any_sync(0xffffffffu, off)) {
+            if (!wait(&bk->v_full[s], (j / kV) & 1)) break;
+            uint8_t* v = smem + SM::kVRing + s * SM::kTile;
+            if (off) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + row_chunk<D>(t, c)) = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < D / 16; ++c)
+                *reinterpret_cast<uint4*>(v + row_chunk<D>(t, c)) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -1382,15 +1406,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 16) cache_combine_kernel(cons
     return;
   }
   const int slice = static_cast<int>(r) / a.slice_rows, n = static_cast<int>(r) - slice * a.slice_rows;
-  const int tiles = sequence_of<SPARSE>(a, b).tiles;
+  const int tiles = sequence_of<SPARSE, true>(a, b).tiles;
   const int qi = static_cast<int>(r) % a.qcap;
   const bool real = !a.n_q || qi < __ldcg(a.n_q + b);
   int s0 = 0, s1 = -1;
   if (tiles > 0) {
     const int heads = a.Hkv * a.n_slices;
-    const int T = length_of_all<SPARSE>(a) * heads;
+    const int T = length_of_all<SPARSE, true>(a) * heads;
     const int shares = min(a.grid, T);
-    const int x0 = length_before<SPARSE>(a, b) * heads + (kvh * a.n_slices + slice) * unit_length(tiles) + kLead;
+    const int x0 = length_before<SPARSE, true>(a, b) * heads + (kvh * a.n_slices + slice) * unit_length(tiles) + kLead;
     s0 = share_of(x0, T, shares), s1 = share_of(x0 + tiles - 1, T, shares);
   }
   griddep_wait();
