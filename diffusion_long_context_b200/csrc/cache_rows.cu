@@ -46,7 +46,7 @@ struct RowArgs {
   const int32_t* n_rows;
   int table_cols, B, H, L, d, page, n_pages, cap, start;
   int cols;                    // store: pages of L positions
-  int steps;                   // CTAs along the positions of one head (blockIdx.x = head * steps + step)
+  int page_shift, vec_shift;   // log2 of page, and of the vectors (of 8 elements) of a row
   int* dev_err;
 };
 
@@ -59,15 +59,50 @@ __device__ __forceinline__ uint32_t absmax_bits(uint4 v, uint32_t m) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// The codes of eight bf16 under scale s: x / s as the definition has it, so an IEEE division
-// (exact ties between two codes exist in plenty: bf16 has few mantissas).
+// The codes of eight bf16 under scale s, those of the IEEE quotient x / s (exact ties between two
+// codes exist in plenty: bf16 has few mantissas).
+//
+// As divisions the eight were most of a store's instructions. With r the rounded reciprocal,
+// q = x r is off by less than 2 ulp, and q + (x - q s) r, one step of residual correction
+// (Markstein 1990), by less than 2^-45 of x / s before its own rounding. So its code can differ
+// from the quotient's only where x / s lies that close to a midpoint of two floats next to a tie
+// t of two codes. With mantissas as integers that is x = (T 2^a +- 1) s to within 16 units, with
+// T 2^a of 25 bits, T (the tie) of 5 or 8 bits, s of 24, x a multiple of 2^40: s is then
+// u 2^a -+ c with |c| <= 16, and u = T c. But u has one bit less than T, so no s does that (nor
+// below a tie that is a power of two, where s would have to be -c).
+// The bounds on s keep r, q s and every residual that matters normal numbers.
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+  if (s > 0x1p-90f && s < 0x1p90f) {
+    const float r = 1.f / s;
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+      const float2 q = mul2(x, r2);
+      const float2 y = fma2(fma2(q, s2, x), r2, q);
+      if constexpr (FMT == FOCUS_CACHE_E4M3) {
+        c[i] = code2<FMT>(y.x, y.y);
+      } else {
+        // rounded to an integer by adding 1.5 * 2^23
+        const float2 n = add2(y, make_float2(12582912.f, 12582912.f));
+        c[i] = __byte_perm(__float_as_uint(n.x), __float_as_uint(n.y), 0x0040);
+      }
+    }
+    uint2 out = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    if constexpr (FMT == FOCUS_CACHE_E4M3) {
+      // the sign of a zero, which the correction drops
+      out.x |= __byte_perm(w[0], w[1], 0x7531) & 0x80808080u;
+      out.y |= __byte_perm(w[2], w[3], 0x7531) & 0x80808080u;
+    }
+    return out;
+  }
   if (s == 0.f) return make_uint2(0u, 0u);
-  uint2 r;
-  r.x = code2<FMT>(bf16_lo(v.x) / s, bf16_hi(v.x) / s) | (code2<FMT>(bf16_lo(v.y) / s, bf16_hi(v.y) / s) << 16);
-  r.y = code2<FMT>(bf16_lo(v.z) / s, bf16_hi(v.z) / s) | (code2<FMT>(bf16_lo(v.w) / s, bf16_hi(v.w) / s) << 16);
-  return r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = code2<FMT>(bf16_lo(w[i]) / s, bf16_hi(w[i]) / s);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // Eight held codes under a grown scale: the nearest code to (code * s_old) / s.
@@ -97,46 +132,42 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m, int gt, uint32_t* s_re
 
 // ------------------------------------------------------------------ store
 // A group of page * d / 32 threads stores one page of one head; a CTA holds 256 threads or one
-// group. blockIdx.y: keys, values.
+// group. blockIdx.y: head, of the keys and then of the values; blockIdx.z: matrix and sequence (as
+// grid dimensions: the divisions of one number cost as many instructions as the codes).
+// The rows are requested before the page is looked up.
 template <int FMT>
 __global__ void __launch_bounds__(512) cache_store_kernel(const RowArgs a) {
   __shared__ uint32_t s_red[16];
   griddep_wait();
   griddep_launch_dependents();
-  const int kv = blockIdx.y;
-  const int gt = a.page * a.d / 32;                     // threads of a group
-  const int per = blockDim.x / gt;
-  const int t = threadIdx.x % gt;
-  const int mbh = blockIdx.x / a.steps;
-  const int j = (blockIdx.x - mbh * a.steps) * per + threadIdx.x / gt;   // page of the sequence
-  const int cpr = a.d / 8;                              // vectors of a row
-  const int b = mbh / a.H % a.B;
-  int rows = 0, page = -1;                              // rows of this page that are stored
-  if (j < a.cols) {
-    rows = min(a.page, (a.lens ? min(a.lens[b], a.L) : a.L) - j * a.page);
-    if (rows > 0) page = checked_page(a.table, a.table_cols, b, j, a.n_pages, a.dev_err);
-    if (page < 0) rows = 0;
-  }
-  const uint4* src = a.X[kv] + (static_cast<long long>(mbh) * a.L + static_cast<long long>(j) * a.page) * cpr;
+  const int kv = blockIdx.y >= a.H ? 1 : 0, h = blockIdx.y - kv * a.H;
+  const int gshift = a.page_shift + a.vec_shift - 2, gt = 1 << gshift;   // threads of a group
+  const int t = threadIdx.x & (gt - 1);
+  const int mat = blockIdx.z / a.B, b = blockIdx.z - mat * a.B;
+  const int j = blockIdx.x * (blockDim.x >> gshift) + (threadIdx.x >> gshift);   // page of the sequence
+  const int rows = j < a.cols ? min(a.page, (a.lens ? min(a.lens[b], a.L) : a.L) - (j << a.page_shift)) : 0;
+  const int n = rows << a.vec_shift;                    // vectors that are stored (none if negative)
+  const long long mbh = static_cast<long long>(blockIdx.z) * a.H + h;
+  const uint4* src = a.X[kv] + ((mbh * a.L + (static_cast<long long>(j) << a.page_shift)) << a.vec_shift);
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = t + i * gt;
-    v[i] = c < rows * cpr ? __ldcs(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    v[i] = c < n ? __ldcs(src + c) : make_uint4(0u, 0u, 0u, 0u);
   }
+  const int page = rows > 0 ? checked_page(a.table, a.table_cols, b, j, a.n_pages, a.dev_err) : -1;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) m = absmax_bits(v[i], m);
   m = group_max(m, gt, s_red);
-  if (rows <= 0) return;
+  if (page < 0) return;
   const float s = __uint_as_float(m << 16) / CodeTop<FMT>::value;
-  const long long mat = mbh / (a.B * a.H);
-  const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;   // page and head
-  uint2* dst = a.code[kv] + ph * (a.page * cpr);
+  const long long ph = (static_cast<long long>(mat) * a.n_pages + page) * a.H + h;   // page and head
+  uint2* dst = a.code[kv] + (ph << (a.page_shift + a.vec_shift));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = t + i * gt;
-    if (c < rows * cpr) dst[c] = encode8<FMT>(v[i], s);
+    if (c < n) dst[c] = encode8<FMT>(v[i], s);
   }
   if (t == 0) a.scale[kv][ph] = s;
 }
@@ -245,55 +276,47 @@ __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
 }
 
 // ------------------------------------------------------------------ load
-// A CTA loads 8 KB of codes (64 rows of 128 or 128 rows of 64) of one head: two 16-byte vectors
-// a thread, so that 64 KB of reads are in flight on a full SM.
-constexpr int kLoadThreads = 256;
+// A CTA loads 2048 vectors of eight codes (128 rows of 128 elements) of one head, eight to a
+// thread, all requested before the first is used. Eight codes are 16 bytes of the output: with
+// sixteen to a vector, each store of a warp wrote half of the 32-byte sectors it touched.
+constexpr int kLoadThreads = 256, kLoadVecs = 8;
 template <int FMT>
 __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const RowArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int kv = blockIdx.y;
-  const int mbh = blockIdx.x / a.steps, step = blockIdx.x - mbh * a.steps;
-  const int b = mbh / a.H % a.B;
-  const int cpr = a.d / 16;                                      // code vectors of a row
-  const int rows_cta = kLoadThreads * 2 / cpr;
+  const int kv = blockIdx.y >= a.H ? 1 : 0, h = blockIdx.y - kv * a.H;
+  const int mat = blockIdx.z / a.B, b = blockIdx.z - mat * a.B;
   const int n = min(a.L, a.lens[b] - a.start);                   // rows of this sequence
-  const long long mat = mbh / (a.B * a.H);
-  uint4 c[2];
-  float s[2];
-  int row[2];
+  const long long x0 = static_cast<long long>(blockIdx.x) * (kLoadThreads * kLoadVecs) + threadIdx.x;
+  uint2 c[kLoadVecs];
+  float s[kLoadVecs];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = threadIdx.x + i * kLoadThreads;
-    row[i] = step * rows_cta + x / cpr;
-    c[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < kLoadVecs; ++i) {
+    const long long x = x0 + i * kLoadThreads;
+    const int row = static_cast<int>(x >> a.vec_shift);
+    c[i] = make_uint2(0u, 0u);
     s[i] = 0.f;
-    if (row[i] < n) {
-      const int pos = a.start + row[i];
-      const int page = checked_page(a.table, a.table_cols, b, pos / a.page, a.n_pages, a.dev_err);
+    if (row < n) {
+      const int pos = a.start + row;
+      const int page = checked_page(a.table, a.table_cols, b, pos >> a.page_shift, a.n_pages, a.dev_err);
       if (page >= 0) {
-        const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;
-        c[i] = __ldcs(reinterpret_cast<const uint4*>(a.code[kv]) + (ph * a.page + pos % a.page) * cpr + x % cpr);
+        const long long ph = (static_cast<long long>(mat) * a.n_pages + page) * a.H + h;
+        c[i] = __ldcs(a.code[kv] + (((ph << a.page_shift) + (pos & (a.page - 1))) << a.vec_shift) +
+                      (x & ((1 << a.vec_shift) - 1)));
         s[i] = a.scale[kv][ph];
       }
     }
   }
+  uint4* dst = a.out[kv] + (((static_cast<long long>(blockIdx.z) * a.H + h) * a.L) << a.vec_shift);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (row[i] >= n) continue;
-    const int x = threadIdx.x + i * kLoadThreads;
-    uint32_t w[8];
-    const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float f[4];
-      decode4<FMT>(in[j], f);
-      w[2 * j] = pack_bf16x2(f[0] * s[i], f[1] * s[i]);
-      w[2 * j + 1] = pack_bf16x2(f[2] * s[i], f[3] * s[i]);
-    }
-    uint4* dst = a.out[kv] + ((static_cast<long long>(mbh) * a.L + row[i]) * cpr + x % cpr) * 2;
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int i = 0; i < kLoadVecs; ++i) {
+    const long long x = x0 + i * kLoadThreads;
+    if (static_cast<int>(x >> a.vec_shift) >= n) continue;
+    float f[4], g[4];
+    decode4<FMT>(c[i].x, f);
+    decode4<FMT>(c[i].y, g);
+    __stcs(dst + x, make_uint4(pack_bf16x2(f[0] * s[i], f[1] * s[i]), pack_bf16x2(f[2] * s[i], f[3] * s[i]),
+                               pack_bf16x2(g[0] * s[i], g[1] * s[i]), pack_bf16x2(g[2] * s[i], g[3] * s[i])));
   }
 }
 
@@ -355,8 +378,17 @@ RowArgs row_args(const focus_cache* c, const int32_t* table, int table_cols, con
   a.d = c->d;
   a.page = c->page;
   a.n_pages = c->n_pages;
+  a.page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  a.vec_shift = c->d == 128 ? 4 : 3;
   a.dev_err = device_error_word();
   return a;
+}
+
+// Grids of (positions, keys' and values' heads, matrix and sequence).
+int check_grid(long long units, int H, const char* what) {
+  if (units <= 65535 && H <= 32767) return FOCUS_OK;
+  set_error("%s: n_mat * B = %lld exceeds 65535 or Hkv = %d 32767", what, units, H);
+  return FOCUS_ERR_UNSUPPORTED;
 }
 
 int launched(cudaError_t e, const char* what) {
@@ -387,12 +419,11 @@ extern "C" int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B
   a.L = L;
   a.cols = (L + a.page - 1) / a.page;
   const int gt = a.page * a.d / 32, threads = std::max(256, gt), per = threads / gt;
-  a.steps = (a.cols + per - 1) / per;
-  const long long blocks = static_cast<long long>(cache->n_mat) * B * a.H * a.steps;
-  if (blocks == 0) return FOCUS_OK;
-  FOCUS_CHECK_ARG(blocks < (1LL << 31), "too large");
+  const long long units = static_cast<long long>(cache->n_mat) * B;
+  if (units == 0) return FOCUS_OK;
+  if (const int st = check_grid(units, a.H, "cache_store")) return st;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_store_kernel<FOCUS_CACHE_E4M3> : cache_store_kernel<FOCUS_CACHE_INT8>;
-  return launched(launch_k(kern, dim3(static_cast<unsigned>(blocks), 2), dim3(threads), 0,
+  return launched(launch_k(kern, dim3((a.cols + per - 1) / per, 2 * a.H, static_cast<unsigned>(units)), dim3(threads), 0,
                            static_cast<cudaStream_t>(stream), a),
                   "cache_store");
 }
@@ -441,13 +472,13 @@ extern "C" int focus_cache_load(const focus_cache* cache, const int32_t* table, 
   a.out[1] = reinterpret_cast<uint4*>(V);
   a.start = start;
   a.L = L;
-  const int rows_cta = kLoadThreads * 2 / (a.d / 16);
-  a.steps = (L + rows_cta - 1) / rows_cta;
-  const long long blocks = static_cast<long long>(cache->n_mat) * B * a.H * a.steps;
-  if (blocks == 0) return FOCUS_OK;
-  FOCUS_CHECK_ARG(blocks < (1LL << 31), "too large");
+  const long long units = static_cast<long long>(cache->n_mat) * B;
+  if (units == 0) return FOCUS_OK;
+  if (const int st = check_grid(units, a.H, "cache_load")) return st;
+  const long long vecs = static_cast<long long>(L) << a.vec_shift, per = kLoadThreads * kLoadVecs;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_load_kernel<FOCUS_CACHE_E4M3> : cache_load_kernel<FOCUS_CACHE_INT8>;
-  return launched(launch_k(kern, dim3(static_cast<unsigned>(blocks), 2), dim3(kLoadThreads), 0,
+  return launched(launch_k(kern, dim3(static_cast<unsigned>((vecs + per - 1) / per), 2 * a.H, static_cast<unsigned>(units)),
+                           dim3(kLoadThreads), 0,
                            static_cast<cudaStream_t>(stream), a),
                   "cache_load");
 }
