@@ -101,12 +101,13 @@ def _check(status: int, name: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:                   # (torch.cuda.current_stream() builds an object: 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t, dtype, name, ndim=None):
@@ -336,7 +337,7 @@ def _here(name, *tensors):
     """The tensors of a call lie on the current device (whose stream and error word it uses)."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"{name}: tensor on {t.device}, the current device is cuda:{cur}")
 
 
