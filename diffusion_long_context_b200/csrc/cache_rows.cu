@@ -105,16 +105,37 @@ __device__ __forceinline__ uint2 encode8(uint4 v, float s) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Eight held codes under a grown scale: the nearest code to (code * s_old) / s.
+// Eight held codes under a grown scale: the codes of the IEEE quotients (code * s_old) / s. Two
+// residual corrections here: the first leaves a faithful quotient, from which the second gives
+// the IEEE one (Markstein 1990), since the dividend has all 24 bits.
 template <int FMT>
-__device__ __forceinline__ uint2 recode8(uint2 c, float s_old, float s) {
-  float x[4], y[4];
-  decode4<FMT>(c.x, x);
-  decode4<FMT>(c.y, y);
-  uint2 r;
-  r.x = code2<FMT>(x[0] * s_old / s, x[1] * s_old / s) | (code2<FMT>(x[2] * s_old / s, x[3] * s_old / s) << 16);
-  r.y = code2<FMT>(y[0] * s_old / s, y[1] * s_old / s) | (code2<FMT>(y[2] * s_old / s, y[3] * s_old / s) << 16);
-  return r;
+__device__ __forceinline__ uint2 recode8(uint2 held, float s_old, float s) {
+  const uint32_t w[2] = {held.x, held.y};
+  uint32_t out[2];
+  const bool scaled = s_old > 0x1p-60f && s < 0x1p60f;     // (s_old < s; every step a normal number)
+  const float r = 1.f / s;
+  const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s), o2 = make_float2(s_old, s_old);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[4];
+    decode4<FMT>(w[i], x);
+    uint32_t c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 y = mul2(make_float2(x[2 * e], x[2 * e + 1]), o2);
+      if (scaled) {
+        float2 q = mul2(y, r2);
+        q = fma2(fma2(q, s2, y), r2, q);
+        q = fma2(fma2(q, s2, y), r2, q);
+        c[e] = code2<FMT>(q.x, q.y);
+      } else {
+        c[e] = code2<FMT>(y.x / s, y.y / s);
+      }
+    }
+    out[i] = c[0] | (c[1] << 16);
+    if (FMT == FOCUS_CACHE_E4M3) out[i] |= w[i] & 0x80808080u;      // the sign of a zero
+  }
+  return make_uint2(out[0], out[1]);
 }
 
 // Largest of `m` over the group of `gt` threads (whole warps) that works on one page; every
@@ -178,28 +199,30 @@ constexpr int kMaxCap = 4096;
 // The CTAs (x = split, y = (mat, b, h), z = keys/values) of one head share the pages that its
 // rows fall in: the first listed row of a page leads, leader number n goes to split n mod
 // gridDim.x. A page is then rebuilt as in the store, from the new rows and the held codes.
+// (The lists lie in dynamic shared memory, as long as the call's cap: with room for the longest
+// always, six CTAs fitted an SM.)
 template <int FMT>
 __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
+  extern __shared__ int s_pos[];         // [cap] position of each listed row, -1 = not written
+  int* const s_lead = s_pos + a.cap;     // [cap] the leaders of this CTA
   __shared__ uint32_t s_red[16];
-  __shared__ int s_col[kMaxCap];         // page column of each listed row, -1 = not written
   __shared__ int s_src[128];             // row of the page -> listed row, -1 = none
-  __shared__ int s_lead[kMaxCap];        // the leaders of this CTA
   __shared__ int s_nlead, s_count[16], s_base;
   griddep_wait();
   griddep_launch_dependents();
   const int kv = blockIdx.z;
   const int mbh = blockIdx.y;
-  const int b = mbh / a.H % a.B;
+  const int mb = mbh / a.H, h = mbh - mb * a.H, mat = mb / a.B, b = mb - mat * a.B;
   const int n = max(0, min(a.n_rows[b], a.cap));
   const int len = a.lens[b];
   const int32_t* rows = a.rows + static_cast<size_t>(b) * a.cap;
-  const int cpr = a.d / 8, gt = blockDim.x, t = threadIdx.x;
+  const int gt = blockDim.x, t = threadIdx.x, ps = a.page_shift;
   bool sorted = true;
   for (int i = t; i < n; i += gt) {
     const int r = rows[i];
-    const bool ok = r >= 0 && r / a.page < a.table_cols;
+    const bool ok = r >= 0 && (r >> ps) < a.table_cols;
     if (!ok) record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
-    s_col[i] = ok ? r / a.page : -1;
+    s_pos[i] = ok ? r : -1;
     sorted = sorted && ok && (i == 0 || rows[i - 1] < r);
   }
   if (t == 0) {
@@ -210,10 +233,10 @@ __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
   // leaders in the order of the list, numbered by a scan over chunks of the CTA
   for (int i0 = 0; i0 < n; i0 += gt) {
     const int i = i0 + t;
-    bool lead = i < n && s_col[i] >= 0;
-    if (lead && sorted) lead = i == 0 || s_col[i - 1] != s_col[i];
+    bool lead = i < n && s_pos[i] >= 0;
+    if (lead && sorted) lead = i == 0 || s_pos[i - 1] >> ps != s_pos[i] >> ps;
     else if (lead)
-      for (int j = 0; j < i && lead; ++j) lead = s_col[j] != s_col[i];
+      for (int j = 0; j < i && lead; ++j) lead = s_pos[j] < 0 || s_pos[j] >> ps != s_pos[i] >> ps;
     const unsigned bal = __ballot_sync(0xffffffffu, lead);
     if (lane_id() == 0) s_count[warp_id()] = __popc(bal);
     __syncthreads();
@@ -230,45 +253,58 @@ __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
     __syncthreads();
   }
   const int nlead = s_nlead;
-  const long long mat = mbh / (a.B * a.H);
   for (int l = 0; l < nlead; ++l) {
-    const int first = s_lead[l], col = s_col[first];
+    const int first = s_lead[l], col = s_pos[first] >> ps, p0 = col << ps;
     __syncthreads();                     // the previous page's s_src has been read
-    for (int r = t; r < a.page; r += gt) {
-      // the last listed row of each position
-      int src = -1;
-      const int last = sorted ? min(n, first + a.page) : n;
-      for (int i = first; i < last; ++i)
-        if (s_col[i] == col && rows[i] - col * a.page == r) src = i;
-      s_src[r] = src;
+    // the last listed row of each position
+    if (sorted) {
+      for (int r = t; r < a.page; r += gt) s_src[r] = -1;
+      __syncthreads();
+      for (int i = first + t; i < min(n, first + a.page); i += gt)
+        if (s_pos[i] >> ps == col) s_src[s_pos[i] - p0] = i;
+    } else {
+      for (int r = t; r < a.page; r += gt) {
+        int src = -1;
+        for (int i = first; i < n; ++i)
+          if (s_pos[i] == p0 + r) src = i;
+        s_src[r] = src;
+      }
     }
     const int page = checked_page(a.table, a.table_cols, b, col, a.n_pages, a.dev_err);
     __syncthreads();
     if (page < 0) continue;              // the same for the whole CTA
-    const long long ph = (mat * a.n_pages + page) * a.H + mbh % a.H;
-    const bool held = col * a.page < len;
+    const long long ph = (static_cast<long long>(mat) * a.n_pages + page) * a.H + h;
+    const bool held = p0 < len;
     const float s_old = held ? a.scale[kv][ph] : 0.f;
+    const uint4* X = a.X[kv] + ((static_cast<long long>(mbh) * a.cap) << a.vec_shift);
+    const int in_row = t & ((1 << a.vec_shift) - 1);       // (gt is a multiple of a row's vectors)
     uint4 v[4];
     int src[4];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c = t + i * gt;          // vector of the page: row c / cpr
-      src[i] = s_src[c / cpr];
+      src[i] = s_src[(t + i * gt) >> a.vec_shift];         // of vector t + i gt of the page
       v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (src[i] >= 0) v[i] = __ldg(a.X[kv] + (static_cast<long long>(mbh) * a.cap + src[i]) * cpr + c % cpr);
+      if (src[i] >= 0) v[i] = __ldg(X + (static_cast<long long>(src[i]) << a.vec_shift) + in_row);
       m = absmax_bits(v[i], m);
     }
     m = group_max(m, gt, s_red);         // (its barriers also order the read of s_old before the write below)
     const float s_new = __uint_as_float(m << 16) / CodeTop<FMT>::value;
     const bool grown = !(s_new <= s_old) && s_old == s_old;      // a NaN stays what it is
     const float s = grown ? s_new : s_old;
-    uint2* dst = a.code[kv] + ph * (a.page * cpr);
+    uint2* dst = a.code[kv] + (ph << (ps + a.vec_shift));
+    uint2 old[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = t + i * gt;
-      if (src[i] >= 0) dst[c] = encode8<FMT>(v[i], s);
-      else if (held && grown && col * a.page + c / cpr < len) dst[c] = recode8<FMT>(dst[c], s_old, s);
+      const bool again = src[i] < 0 && held && grown && p0 + (c >> a.vec_shift) < len;
+      if (again) old[i] = dst[c];
+      else if (src[i] < 0) src[i] = -2;  // stays as it is
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (src[i] >= 0) dst[t + i * gt] = encode8<FMT>(v[i], s);
+      else if (src[i] == -1) dst[t + i * gt] = recode8<FMT>(old[i], s_old, s);
     }
     __syncthreads();                     // every thread has read s_old
     if (t == 0) a.scale[kv][ph] = s;
@@ -455,7 +491,8 @@ extern "C" int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf
   const int splits = std::min(16, (cap + a.page - 1) / a.page + 1);
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3>
                                                 : cache_scatter_kernel<FOCUS_CACHE_INT8>;
-  return launched(launch_k(kern, dim3(splits, static_cast<unsigned>(units), 2), dim3(a.page * a.d / 32), 0,
+  return launched(launch_k(kern, dim3(splits, static_cast<unsigned>(units), 2), dim3(a.page * a.d / 32),
+                           2 * sizeof(int) * static_cast<size_t>(cap),
                            static_cast<cudaStream_t>(stream), a),
                   "cache_scatter_rows");
 }
