@@ -487,8 +487,10 @@ extern "C" int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf
   a.rows = rows;
   a.n_rows = n_rows;
   a.cap = cap;
-  // rows next to each other fall in cap / page + 1 pages or fewer
-  const int splits = std::min(16, (cap + a.page - 1) / a.page + 1);
+  // rows next to each other fall in cap / page + 1 pages or fewer; no more CTAs to a head than fill
+  // the GPU eight times
+  const long long fill = (static_cast<long long>(device_sm_count()) * 8 + 2 * units - 1) / (2 * units);
+  const int splits = static_cast<int>(std::min<long long>(std::min(16, (cap + a.page - 1) / a.page + 1), fill));
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3>
                                                 : cache_scatter_kernel<FOCUS_CACHE_INT8>;
   return launched(launch_k(kern, dim3(splits, static_cast<unsigned>(units), 2), dim3(a.page * a.d / 32),
