@@ -199,9 +199,10 @@ struct __align__(16) Book {
   alignas(16) float q_scale[2][NQ];
   alignas(16) float top[kS][4][NQ];            // [S buffer][warp][column]: largest score, without the query's scale
   alignas(16) float qs[8][NQ];                 // [exp warp][column]: scale of the query
-  // of a tile's columns, [entry][column], bf16: -reference of its probabilities, factor from that
-  // to the run's reference, and the run's reference
-  alignas(16) uint16_t ref[kE][NQ], be[kE][NQ], run[kE][NQ];
+  // of a tile's columns, [entry][column]: -reference of its probabilities, the run's reference, and
+  // the factor from one to the other, a power of two, in bf16
+  alignas(16) float ref[kE][NQ], run[kE][NQ];
+  alignas(16) uint16_t be[kE][NQ];
   float o_vmax[kE];                                // and its value scale
   float x_m[2][2][NQ], x_l[2][8][NQ];      // [run parity]: reference, row sums of the exp warps
   int blk[kProducers][kMaxList], snk[kProducers][kMaxList];   // a producer's lists of its unit
@@ -1005,31 +1006,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rb = jr % kS;
         if (jr < j && test(&bk->t_full[rb], (jr / kS) & 1)) {
           // A tile's probabilities are relative to a reference of its own, the next whole number
-          // (that bf16 holds) above its largest score in units of log2. (Against a running maximum
-          // instead, all that lies 2^-18 below one large key, an attention sink, would be rounded
-          // away, and with thousands of such keys a part of the result; so, no more than
-          // 128 * 2^-18 of a tile's own largest is, or 2^-17.) Sums over tiles are relative to
-          // m_ref, the reference of the run's first tile with keys, which moves up only when another
-          // is above it by 30: fp32 has the range, no sum is rescaled tile by tile, and the factor
-          // between the two is an exact power of two. Whole numbers make all three 16 bits wide:
-          // handing them to all threads costs shared-memory bandwidth, of which the tensor cores
-          // take half.
+          // above its largest score in units of log2. (Against a running maximum instead, all that
+          // lies 2^-18 below one large key, an attention sink, would be rounded away, and with
+          // thousands of such keys a part of the result.) Sums over tiles are relative to m_ref, the
+          // reference of the run's first tile with keys, which moves up only when another is above
+          // it by 30: fp32 has the range, no sum is rescaled tile by tile, and the factor between
+          // the two, a power of two, is exact in 16 bits: handing it to all threads costs
+          // shared-memory bandwidth, of which the tensor cores take half. (The reference itself
+          // takes all 32: rounded up to bf16 too, it lay 2^5 above scores of some thousands.)
           const float* tp = &bk->top[rb][0][lc];
           const float mt = max3_nan(max_nan(tp[0], tp[NQ]), tp[2 * NQ], tp[3 * NQ]);
-          uint32_t r16 = 0;                      // bf16 of the reference
-          uint32_t be16 = 0;                     // and of the factor
-          if (mt != -INFINITY) {                 // (a tile without keys adds nothing)
-            const uint32_t c = __float_as_uint(ceilf(mt * qs));
-            r16 = mt != mt ? 0x7fc0u : (c & 0x80000000u) ? c >> 16 : (c + 0xffffu) >> 16;
-            const float ref = __uint_as_float(r16 << 16);
+          float ref = 0.f;                       // (a tile without keys adds nothing)
+          uint32_t be16 = 0;                     // bf16 of the factor
+          if (mt != -INFINITY) {
+            ref = ceilf(mt * qs);
             if (ref > m_ref + 30.f || m_ref == -INFINITY) m_ref = ref;
             const float e = ref - m_ref;         // a whole number
             be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
           }
           const int e = jr % kE;
-          bk->ref[e][lc] = static_cast<uint16_t>(r16 ^ 0x8000u);
+          bk->ref[e][lc] = -ref;
           bk->be[e][lc] = static_cast<uint16_t>(be16);
-          bk->run[e][lc] = static_cast<uint16_t>(__float_as_uint(m_ref) >> 16);
+          bk->run[e][lc] = m_ref;
           if (lane == 0) bk->o_vmax[e] = bk->vmax[jr % kV];
           __syncwarp();
           if (lane == 0) mbar_arrive(&bk->m_full[rb]);
@@ -1191,7 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           bool off;
           const float2 key = key_of(s, off);
-          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[e][lc]) << 16);
+          const float m_new = bk->run[e][lc];
           if (__any_sync(0xffffffffu, m_new != m_ref)) {               // (the run's first tile, seldom another)
             scale_columns<NQ>(tl, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
             m_ref = m_new;
@@ -1220,11 +1218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               float2 x0 = mul2(both2<FMT>(r + 4 * i, r2 + 4 * i), make_float2(key.x, key.x));
               float2 x1 = mul2(both2<FMT>(r + 4 * i + 2, r2 + 4 * i + 2), make_float2(key.x, key.x));
               if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
-              const uint2 rv = *reinterpret_cast<const uint2*>(&bk->ref[e][h + 4 * i]);
+              const float4 rv = *reinterpret_cast<const float4*>(&bk->ref[e][h + 4 * i]);
               const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[e][h + 4 * i]);
               const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[we][h + 4 * i]);
-              float2 p0 = fma2(x0, make_float2(qv.x, qv.y), bf16_pair(rv.x));
-              float2 p1 = fma2(x1, make_float2(qv.z, qv.w), bf16_pair(rv.y));
+              float2 p0 = fma2(x0, make_float2(qv.x, qv.y), make_float2(rv.x, rv.y));
+              float2 p1 = fma2(x1, make_float2(qv.z, qv.w), make_float2(rv.z, rv.w));
               p0 = make_float2(exp2_approx(p0.x), exp2_approx(p0.y));
               p1 = make_float2(exp2_approx(p1.x), exp2_approx(p1.y));
               const float2 l0 = fma2(p0, bf16_pair(bv.x), make_float2(__uint_as_float(rl[4 * i]), __uint_as_float(rl[4 * i + 1])));
@@ -1287,7 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(&bk->o_full[ob], (j / kO) & 1)) break;
           tc_fence_after();
           const float2 vmax = make_float2(bk->o_vmax[e], bk->o_vmax[e]);
-          const float m_new = __uint_as_float(static_cast<uint32_t>(bk->run[e][lc]) << 16);
+          const float m_new = bk->run[e][lc];
           if (__any_sync(0xffffffffu, m_new != m_ref)) {
             scale_columns<NQ>(ta, m_new == m_ref ? 1.f : exp2_approx(m_ref - m_new), false);
             m_ref = m_new;

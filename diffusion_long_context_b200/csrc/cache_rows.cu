@@ -133,7 +133,7 @@ __device__ __forceinline__ uint2 recode8(uint2 held, float s_old, float s) {
       }
     }
     out[i] = c[0] | (c[1] << 16);
-    if (FMT == FOCUS_CACHE_E4M3) out[i] |= w[i] & 0x80808080u;      // the sign of a zero
+    if (FMT == FOCUS_CACHE_E4M3 && scaled) out[i] |= w[i] & 0x80808080u;      // the sign of a zero
   }
   return make_uint2(out[0], out[1]);
 }
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(512) cache_store_kernel(const RowArgs a) {
   const int t = threadIdx.x & (gt - 1);
   const int mat = blockIdx.z / a.B, b = blockIdx.z - mat * a.B;
   const int j = blockIdx.x * (blockDim.x >> gshift) + (threadIdx.x >> gshift);   // page of the sequence
-  const int rows = j < a.cols ? min(a.page, (a.lens ? min(a.lens[b], a.L) : a.L) - (j << a.page_shift)) : 0;
+  const int rows = j < a.cols ? min(a.page, (a.lens ? max(0, min(a.lens[b], a.L)) : a.L) - (j << a.page_shift)) : 0;
   const int n = rows << a.vec_shift;                    // vectors that are stored (none if negative)
   const long long mbh = static_cast<long long>(blockIdx.z) * a.H + h;
   const uint4* src = a.X[kv] + ((mbh * a.L + (static_cast<long long>(j) << a.page_shift)) << a.vec_shift);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const RowArgs 
   griddep_launch_dependents();
   const int kv = blockIdx.y >= a.H ? 1 : 0, h = blockIdx.y - kv * a.H;
   const int mat = blockIdx.z / a.B, b = blockIdx.z - mat * a.B;
-  const int n = min(a.L, a.lens[b] - a.start);                   // rows of this sequence
+  const int n = min(a.L, max(0, a.lens[b]) - a.start);                   // rows of this sequence
   const long long x0 = static_cast<long long>(blockIdx.x) * (kLoadThreads * kLoadVecs) + threadIdx.x;
   uint2 c[kLoadVecs];
   float s[kLoadVecs];
@@ -449,15 +449,15 @@ extern "C" int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B
   if (const int st = check_cache(cache, table, table_cols, false)) return st;
   FOCUS_CHECK_ARG(B >= 0 && L >= 1, "bad sizes (B=%d L=%d)", B, L);
   FOCUS_CHECK_ARG(aligned16(K) && aligned16(V), "tensors must be 16-byte aligned");
+  const long long units = static_cast<long long>(cache->n_mat) * B;
+  if (units == 0) return FOCUS_OK;
+  if (const int st = check_grid(units, cache->Hkv, "cache_store")) return st;
   RowArgs a = row_args(cache, table, table_cols, lens, B);
   a.X[0] = reinterpret_cast<const uint4*>(K);
   a.X[1] = reinterpret_cast<const uint4*>(V);
   a.L = L;
   a.cols = (L + a.page - 1) / a.page;
   const int gt = a.page * a.d / 32, threads = std::max(256, gt), per = threads / gt;
-  const long long units = static_cast<long long>(cache->n_mat) * B;
-  if (units == 0) return FOCUS_OK;
-  if (const int st = check_grid(units, a.H, "cache_store")) return st;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_store_kernel<FOCUS_CACHE_E4M3> : cache_store_kernel<FOCUS_CACHE_INT8>;
   return launched(launch_k(kern, dim3((a.cols + per - 1) / per, 2 * a.H, static_cast<unsigned>(units)), dim3(threads), 0,
                            static_cast<cudaStream_t>(stream), a),
@@ -506,14 +506,14 @@ extern "C" int focus_cache_load(const focus_cache* cache, const int32_t* table, 
   FOCUS_CHECK_ARG(B >= 0 && L >= 1 && start >= 0 && static_cast<long long>(start) + L < (1LL << 31),
                   "bad sizes (B=%d start=%d L=%d)", B, start, L);
   FOCUS_CHECK_ARG(aligned16(K) && aligned16(V), "tensors must be 16-byte aligned");
+  const long long units = static_cast<long long>(cache->n_mat) * B;
+  if (units == 0) return FOCUS_OK;
+  if (const int st = check_grid(units, cache->Hkv, "cache_load")) return st;
   RowArgs a = row_args(cache, table, table_cols, lens, B);
   a.out[0] = reinterpret_cast<uint4*>(K);
   a.out[1] = reinterpret_cast<uint4*>(V);
   a.start = start;
   a.L = L;
-  const long long units = static_cast<long long>(cache->n_mat) * B;
-  if (units == 0) return FOCUS_OK;
-  if (const int st = check_grid(units, a.H, "cache_load")) return st;
   const long long vecs = static_cast<long long>(L) << a.vec_shift, per = kLoadThreads * kLoadVecs;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_load_kernel<FOCUS_CACHE_E4M3> : cache_load_kernel<FOCUS_CACHE_INT8>;
   return launched(launch_k(kern, dim3(static_cast<unsigned>((vecs + per - 1) / per), 2 * a.H, static_cast<unsigned>(units)),

@@ -309,6 +309,7 @@ typedef struct {
  * scales are set anew. K, V [n_mat, B, Hkv, L, d] bf16; lens [B] int32 (device, clamped to
  * [0, L]) or NULL for L. Positions behind lens[b] keep their codes (in the last page, under
  * that page's new scale). One pass: every element is read once and every code written once.
+ * Requires n_mat * B <= 65535.
  */
 FOCUS_API int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B, int L, const int32_t* lens,
                                 const int32_t* table, int table_cols, const focus_cache* cache, void* stream);
@@ -322,7 +323,8 @@ FOCUS_API int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B,
  * top); when it does, its other held rows are coded again, the nearest code to
  * (code * s) / s' (product and quotient rounded in fp32). A page that starts at or behind
  * lens[b] held nothing: s' = max|new| / top. Other positions behind lens[b] keep their codes.
- * Negative rows are flagged like positions behind the table. Requires 1 <= cap <= 4096.
+ * Negative rows are flagged like positions behind the table. Requires 1 <= cap <= 4096 and
+ * n_mat * B * Hkv <= 65535.
  */
 FOCUS_API int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf16* V_rows, const int32_t* rows,
                                        const int32_t* n_rows, int B, int cap, const int32_t* lens,
@@ -331,7 +333,8 @@ FOCUS_API int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf1
 /*
  * Positions [start, min(start + L, lens[b])) of the cache as bf16: K[m, b, h, i] = code * scale
  * of position start + i, rounded once; K, V [n_mat, B, Hkv, L, d]. Rows behind lens[b] are left
- * as they were. start >= 0; lens as in focus_cache_store, but not clamped to L.
+ * as they were. start >= 0; lens as in focus_cache_store, but not clamped to L. Requires
+ * n_mat * B <= 65535.
  */
 FOCUS_API int focus_cache_load(const focus_cache* cache, const int32_t* table, int table_cols, const int32_t* lens,
                                int B, int start, int L, focus_bf16* K, focus_bf16* V, void* stream);

@@ -166,3 +166,15 @@ def test_the_binding_refuses_what_does_not_fit(F):
     with pytest.raises(ValueError):
         F.Pages(torch.zeros(4, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32),
                 torch.zeros(2, dtype=torch.int32))
+
+
+def test_more_heads_than_a_grid_holds_are_refused(F):
+    lib, before = F.lib, F.lib.focus_launch_count()
+    many = ctypes.byref(_cache(F, n_mat=300))
+    assert lib.focus_cache_store(FAKE, FAKE, 219, 64, None, FAKE, 1, many, None) == -2
+    assert lib.focus_cache_load(many, FAKE, 1, FAKE, 219, 0, 64, FAKE, FAKE, None) == -2
+    assert lib.focus_cache_scatter_rows(FAKE, FAKE, FAKE, FAKE, 55, 8, FAKE, FAKE, 1, many, None) == -2
+    wide = ctypes.byref(_cache(F, Hkv=32768))
+    assert lib.focus_cache_store(FAKE, FAKE, 1, 64, None, FAKE, 1, wide, None) == -2
+    assert lib.focus_cache_load(wide, FAKE, 1, FAKE, 1, 0, 64, FAKE, FAKE, None) == -2
+    assert lib.focus_launch_count() == before
