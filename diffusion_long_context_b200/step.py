@@ -8,6 +8,10 @@ A non-block-entry step (Focus-dLLM summary page, "方法步骤详情" / method s
 A block-entry step refreshes the block means of every sparse layer (and, for the
 comparison, runs the dense full refresh).
 
+With `cache` the keys and values of all layers are held in 8 bits, in pages of one prompt block:
+block entry stores them, the layers read them from there, refresh_rows() replaces the rows that
+a step has projected anew.
+
 This module only allocates buffers and orders the calls on one CUDA stream; every
 step of the computation runs in libfocus.so kernels. `SparseStep.capture()` records
 the whole step into a CUDA graph so that replay costs one launch from the host.
@@ -25,13 +29,17 @@ from .configs import FocusConfig
 
 class SparseStep:
     def __init__(self, cfg: FocusConfig, Q_full: torch.Tensor, K: List[torch.Tensor], V: List[torch.Tensor],
-                 device="cuda", fused: bool = True):
+                 device="cuda", fused: bool = True, cache: Optional[torch.dtype] = None):
         """Q_full [n_layers, B, Hq, L, d]; K[l], V[l] [B, Hkv, L, d] (bf16, on `device`).
 
         fused: each sparse layer runs block relevance + top-C and the sparse attention as
         one launch (focus_sparse_attention_fused), else as two calls. The config's variants
         (dense_tail, relevance, sink_agg) change the schedule; relevance="focus" runs the
-        two calls."""
+        two calls.
+
+        cache: torch.float8_e4m3fn or torch.int8, hold keys and values in the 8-bit paged cache.
+        K and V are then what block_entry() stores; the steps read the cache alone (the layer
+        that finds the sinks through one bf16 copy of its rows), each sparse layer by two calls."""
         c = cfg
         self.cfg = c
         self.fused = fused
@@ -68,10 +76,41 @@ class SparseStep:
         self.blocks = {l: torch.full((c.B, c.Hkv, c.C), -1, **i32) for l in self.sparse_layers}
         dws = F.dense_workspace_bytes(c.B, c.Hq, c.Hkv, c.L, c.d, c.acap, True)
         sws = F.sparse_workspace_bytes(c.B, c.Hq, c.Hkv, c.L, c.d, c.acap, c.S, c.C, c.bs, c.P, c.g0, c.g1)
-        self.ws = torch.empty(max(dws, sws, 256), dtype=torch.uint8, device=self.dev)
+        cws = F.cache_workspace_bytes(c.B, c.Hq, c.Hkv, c.d, c.acap) if cache is not None else 0
+        self.ws = torch.empty(max(dws, sws, cws, 256), dtype=torch.uint8, device=self.dev)
+        self.cache = None
+        if cache is not None:
+            self._make_cache(cache)
         self.graph: Optional[torch.cuda.CUDAGraph] = None
         self.graph_io: Optional[torch.cuda.CUDAGraph] = None
         self.launches_per_step: Optional[int] = None
+
+    # ------------------------------------------------------------------ 8-bit cache
+    def _make_cache(self, fmt: torch.dtype):
+        c = self.cfg
+        if fmt not in F.CACHE_FORMATS:
+            raise TypeError("cache must be torch.float8_e4m3fn or torch.int8")
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        cols = -(-c.L // c.bs)
+        codes = (c.n_layers, c.B * cols, c.Hkv, c.bs, c.d)
+
+        def tensors(dtype, shape):
+            return torch.zeros(shape, dtype=dtype, device=self.dev)
+        self.cache = F.Cache(tensors(torch.uint8, codes).view(fmt), tensors(torch.uint8, codes).view(fmt),
+                             tensors(torch.float32, codes[:3]), tensors(torch.float32, codes[:3]))
+        self.cache_layers = [self.cache.layer(l) for l in range(c.n_layers)]
+        self.table = torch.arange(c.B * cols, **i32).view(c.B, cols)
+        self.lens = torch.full((c.B,), c.L, **i32)
+        self.P_seq, self.g0_seq = torch.full((c.B,), c.P, **i32), torch.full((c.B,), c.g0, **i32)
+        self.K_sink, self.V_sink = (torch.empty((c.B, c.Hkv, c.L, c.d), dtype=torch.bfloat16, device=self.dev)
+                                    for _ in range(2))
+        self.fused = False
+
+    def refresh_rows(self, K_rows: torch.Tensor, V_rows: torch.Tensor):
+        """The active rows' new keys and values, [n_layers, B, Hkv, acap, d], into the cache."""
+        if self.cache is None:
+            raise ValueError("refresh_rows needs a step with a cache")
+        F.focus_cache_scatter_rows(K_rows, V_rows, self.i_active, self.n_active, self.cache, self.table, self.lens)
 
     # ------------------------------------------------------------------ inputs
     def set_state(self, conf_prev: torch.Tensor, mask: torch.Tensor, non_blocking=True):
@@ -83,8 +122,11 @@ class SparseStep:
         """Block entry. Without O_full: the block means of every sparse layer only (cached for
         the later steps of the block). With O_full [B, Hq, L, d]: the block-entry step proper,
         every layer's dense full refresh into O_full (reused per layer), the sparse layers'
-        block means computed in the same launch."""
+        block means computed in the same launch. With a cache, K and V go into it."""
         c = self.cfg
+        if self.cache is not None:
+            for l in range(c.n_layers):
+                F.focus_cache_store(self.K[l], self.V[l], self.cache_layers[l], self.table)
         if O_full is None:
             for l in self.sparse_layers:
                 F.focus_block_means(self.K[l], c.P, c.bs, self.kbar[l])
@@ -114,17 +156,24 @@ class SparseStep:
     def dense_layer(self, l: int):
         c = self.cfg
         sink_layer = l == c.l_dense
+        K, V = self.K[l], self.V[l]
+        if self.cache is not None:
+            if not sink_layer:
+                F.focus_cache_attention(self.Q_active[l], self.n_active, self.cache_layers[l], self.table, self.lens,
+                                        self.O_active[l], scale=self.scale, ws=self.ws)
+                return
+            K, V = self.K_sink, self.V_sink
+            F.focus_cache_load(self.cache_layers[l], self.table, self.lens, 0, K, V)
         probs = sink_layer and c.sink_agg == "probs"
         if probs:
             # attention, column sums and the top-S sinks in one call (one launch where served)
-            F.focus_dense_attention_sinks(self.Q_active[l], self.n_active, self.K[l], self.V[l], self.O_active[l],
-                                          self.colsum, self.sinks, scale=self.scale, ws=self.ws)
+            F.focus_dense_attention_sinks(self.Q_active[l], self.n_active, K, V, self.O_active[l], self.colsum,
+                                          self.sinks, scale=self.scale, ws=self.ws)
             return
-        F.focus_dense_attention(self.Q_active[l], self.n_active, self.K[l], self.V[l], self.O_active[l],
-                                scale=self.scale, ws=self.ws)
+        F.focus_dense_attention(self.Q_active[l], self.n_active, K, V, self.O_active[l], scale=self.scale, ws=self.ws)
         if sink_layer:
             # mean-query importance: top-S of qbar . k_j over all L keys (each key a block of one)
-            F.focus_block_means(self.K[l], c.L, 1, self.k_rows)
+            F.focus_block_means(K, c.L, 1, self.k_rows)
             F.focus_block_select(self.Q_active[l], self.n_active, self.k_rows, c.S, self.sinks)
 
     def block_select_layer(self, l: int):
@@ -135,6 +184,11 @@ class SparseStep:
 
     def sparse_attention_layer(self, l: int):
         c = self.cfg
+        if self.cache is not None:
+            F.focus_cache_sparse_attention(self.Q_active[l], self.n_active, self.cache_layers[l], self.table, self.P_seq,
+                                           self.g0_seq, c.G, self.sinks, self.blocks[l], self.O_active[l],
+                                           scale=self.scale, ws=self.ws)
+            return
         F.focus_sparse_attention(self.Q_active[l], self.n_active, self.K[l], self.V[l], self.sinks,
                                  self.blocks[l], c.bs, c.P, c.g0, c.g1, self.O_active[l], scale=self.scale,
                                  ws=self.ws)
