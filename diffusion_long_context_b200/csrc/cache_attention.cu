@@ -1125,16 +1125,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp < kExpWarp) {
       // ---------------------------------------------------------- largest scores
+      auto queries = [&](const Desc& x, int qb) {
+        split_queries<FMT, D, NQ>(a, x, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], warp, 4);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&bk->q_full[qb], kQParts / 4);
+      };
+      auto test = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+      bool ready = false;                        // the next run's query rows are there
       for (int di = 0; next_run(di); ++di) {
-        if (di > 0) {
-          // the run's query rows, while the later stages are still at the last run's tiles
-          const int qb = di & 1;
-          if (di >= 2 && !wait(&bk->q_empty[qb], ((di >> 1) - 1) & 1)) break;
-          split_queries<FMT, D, NQ>(a, d, smem + SM::kQ + qb * SM::kQBuf, bk->q_scale[qb], warp, 4);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_n(&bk->q_full[qb], kQParts / 4);
+        // the run's query rows, if there was no time during the run before
+        if (di > 0 && !ready) {
+          if (di >= 2 && !wait(&bk->q_empty[di & 1], ((di >> 1) - 1) & 1)) break;
+          queries(d, di & 1);
         }
+        ready = false;
         for (int j = d.j0; j < d.j0 + d.n; ++j) {
           const int s = j % kV, sb = j % kS;
           if (!wait(&bk->s_full[sb], (j / kS) & 1)) break;   // (and with it the tile's scales and bytes)
@@ -1162,6 +1167,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bk->t_full[sb]);
+          // The next run's 16 query rows, as soon as that run is known and the rows of the one before
+          // this are used up: its scores then follow this run's without a gap (sixteen ragged
+          // sequences: 57 -> 50 us). 32 rows take twice as long, and in mid-run that costs the chain
+          // as much as it saves (four sequences' kept blocks: 36 -> 39 us).
+          if constexpr (NQ == 16) {
+            const int dn = di + 1, ds = dn % kDescs;
+            if (!ready && test(&bk->d_full[ds], (dn / kDescs) & 1) &&
+                (dn < 2 || test(&bk->q_empty[dn & 1], ((dn >> 1) - 1) & 1))) {
+              if (bk->desc[ds].n > 0) queries(bk->desc[ds], dn & 1);
+              ready = true;
+            }
+          }
         }
         if (!ok) break;
       }
