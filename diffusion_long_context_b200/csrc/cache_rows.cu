@@ -199,9 +199,57 @@ constexpr int kMaxCap = 4096;
 // The CTAs (x = split, y = (mat, b, h), z = keys/values) of one head share the pages that its
 // rows fall in: the first listed row of a page leads, leader number n goes to split n mod
 // gridDim.x. A page is then rebuilt as in the store, from the new rows and the held codes.
-// (The lists lie in dynamic shared memory, as long as the call's cap: with room for the longest
-// always, six CTAs fitted an SM.)
+//
+// Bound by its chain of dependent steps, not by bytes. A list of 32 rows at most (one denoising
+// block, SHORT) is a register of each warp: leaders by a match, the row of a position by a
+// ballot, no shared memory and no barriers but those of the largest magnitude (32 rows of 32
+// layers of 32 heads: 16.5 us against 19.3 by the way for longer lists). Longer lists lie
+// in dynamic shared memory, as long as the call's cap (with room for the longest always, six
+// CTAs fitted an SM).
+struct PageRows {                        // what a thread writes of a page: vectors t, t + gt, ...
+  int src[4];                            // listed rows, -1 = none
+};
+
+// Rebuilds one page from the new rows src; the whole CTA.
 template <int FMT>
+__device__ __forceinline__ void rebuild_page(const RowArgs& a, int kv, int mbh, long long ph, int p0, int len, PageRows& w,
+                                             uint32_t* s_red) {
+  const int gt = blockDim.x, t = threadIdx.x;
+  const bool held = p0 < len;
+  const float s_old = held ? a.scale[kv][ph] : 0.f;
+  const uint4* X = a.X[kv] + ((static_cast<long long>(mbh) * a.cap) << a.vec_shift);
+  const int in_row = t & ((1 << a.vec_shift) - 1);         // (gt is a multiple of a row's vectors)
+  uint4 v[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (w.src[i] >= 0) v[i] = __ldg(X + (static_cast<long long>(w.src[i]) << a.vec_shift) + in_row);
+    m = absmax_bits(v[i], m);
+  }
+  m = group_max(m, gt, s_red);
+  const float s_new = __uint_as_float(m << 16) / CodeTop<FMT>::value;
+  const bool grown = !(s_new <= s_old) && s_old == s_old;      // a NaN stays what it is
+  const float s = grown ? s_new : s_old;
+  uint2* dst = a.code[kv] + (ph << (a.page_shift + a.vec_shift));
+  uint2 old[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = t + i * gt;
+    const bool again = w.src[i] < 0 && held && grown && p0 + (c >> a.vec_shift) < len;
+    if (again) old[i] = dst[c];
+    else if (w.src[i] < 0) w.src[i] = -2;                  // stays as it is
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (w.src[i] >= 0) dst[t + i * gt] = encode8<FMT>(v[i], s);
+    else if (w.src[i] == -1) dst[t + i * gt] = recode8<FMT>(old[i], s_old, s);
+  }
+  __syncthreads();                       // every thread has read s_old
+  if (t == 0) a.scale[kv][ph] = s;
+}
+
+template <int FMT, bool SHORT>
 __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
   extern __shared__ int s_pos[];         // [cap] position of each listed row, -1 = not written
   int* const s_lead = s_pos + a.cap;     // [cap] the leaders of this CTA
@@ -217,6 +265,43 @@ __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
   const int len = a.lens[b];
   const int32_t* rows = a.rows + static_cast<size_t>(b) * a.cap;
   const int gt = blockDim.x, t = threadIdx.x, ps = a.page_shift;
+  const long long heads = static_cast<long long>(mat) * a.n_pages;
+  if constexpr (SHORT) {
+    const int lane = lane_id();
+    int pos = -1;
+    if (lane < n) {
+      pos = rows[lane];
+      if (pos < 0 || (pos >> ps) >= a.table_cols) {
+        record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
+        pos = -1;
+      }
+    }
+    const int col_of = pos >> ps;                          // (-1 for what is not written)
+    const unsigned same = __match_any_sync(0xffffffffu, col_of);
+    unsigned leaders = __ballot_sync(0xffffffffu, pos >= 0 && __ffs(same) - 1 == lane);
+    int page_of = -1;
+    if ((leaders >> lane) & 1u) page_of = checked_page(a.table, a.table_cols, b, col_of, a.n_pages, a.dev_err);
+    for (int l = 0; leaders; ++l, leaders &= leaders - 1) {
+      if (l % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
+      const int first = __ffs(leaders) - 1;
+      const int p0 = __shfl_sync(0xffffffffu, col_of, first) << ps, page = __shfl_sync(0xffffffffu, page_of, first);
+      if (page < 0) continue;                              // the same for the whole CTA
+      // a warp's 32 vectors are of 2 rows, or with d = 64 of 4
+      PageRows w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = p0 + ((t + i * gt) >> a.vec_shift);
+        w.src[i] = -1;
+        for (int k = 0; k < 32; k += 1 << a.vec_shift) {
+          const int r = __shfl_sync(0xffffffffu, row, k);
+          const unsigned listed = __ballot_sync(0xffffffffu, pos == r);
+          if (row == r && listed) w.src[i] = 31 - __clz(listed);      // the last listed row of the position
+        }
+      }
+      rebuild_page<FMT>(a, kv, mbh, (heads + page) * a.H + h, p0, len, w, s_red);
+    }
+    return;
+  }
   bool sorted = true;
   for (int i = t; i < n; i += gt) {
     const int r = rows[i];
@@ -273,41 +358,10 @@ __global__ void __launch_bounds__(512) cache_scatter_kernel(const RowArgs a) {
     const int page = checked_page(a.table, a.table_cols, b, col, a.n_pages, a.dev_err);
     __syncthreads();
     if (page < 0) continue;              // the same for the whole CTA
-    const long long ph = (static_cast<long long>(mat) * a.n_pages + page) * a.H + h;
-    const bool held = p0 < len;
-    const float s_old = held ? a.scale[kv][ph] : 0.f;
-    const uint4* X = a.X[kv] + ((static_cast<long long>(mbh) * a.cap) << a.vec_shift);
-    const int in_row = t & ((1 << a.vec_shift) - 1);       // (gt is a multiple of a row's vectors)
-    uint4 v[4];
-    int src[4];
-    uint32_t m = 0;
+    PageRows w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      src[i] = s_src[(t + i * gt) >> a.vec_shift];         // of vector t + i gt of the page
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (src[i] >= 0) v[i] = __ldg(X + (static_cast<long long>(src[i]) << a.vec_shift) + in_row);
-      m = absmax_bits(v[i], m);
-    }
-    m = group_max(m, gt, s_red);         // (its barriers also order the read of s_old before the write below)
-    const float s_new = __uint_as_float(m << 16) / CodeTop<FMT>::value;
-    const bool grown = !(s_new <= s_old) && s_old == s_old;      // a NaN stays what it is
-    const float s = grown ? s_new : s_old;
-    uint2* dst = a.code[kv] + (ph << (ps + a.vec_shift));
-    uint2 old[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = t + i * gt;
-      const bool again = src[i] < 0 && held && grown && p0 + (c >> a.vec_shift) < len;
-      if (again) old[i] = dst[c];
-      else if (src[i] < 0) src[i] = -2;  // stays as it is
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (src[i] >= 0) dst[t + i * gt] = encode8<FMT>(v[i], s);
-      else if (src[i] == -1) dst[t + i * gt] = recode8<FMT>(old[i], s_old, s);
-    }
-    __syncthreads();                     // every thread has read s_old
-    if (t == 0) a.scale[kv][ph] = s;
+    for (int i = 0; i < 4; ++i) w.src[i] = s_src[(t + i * gt) >> a.vec_shift];
+    rebuild_page<FMT>(a, kv, mbh, (heads + page) * a.H + h, p0, len, w, s_red);
   }
 }
 
@@ -491,10 +545,11 @@ extern "C" int focus_cache_scatter_rows(const focus_bf16* K_rows, const focus_bf
   // the GPU eight times
   const long long fill = (static_cast<long long>(device_sm_count()) * 8 + 2 * units - 1) / (2 * units);
   const int splits = static_cast<int>(std::min<long long>(std::min(16, (cap + a.page - 1) / a.page + 1), fill));
-  auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3>
-                                                : cache_scatter_kernel<FOCUS_CACHE_INT8>;
+  const bool e4m3 = cache->format == FOCUS_CACHE_E4M3, few = cap <= 32;
+  auto kern = few ? (e4m3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3, true> : cache_scatter_kernel<FOCUS_CACHE_INT8, true>)
+                  : (e4m3 ? cache_scatter_kernel<FOCUS_CACHE_E4M3, false> : cache_scatter_kernel<FOCUS_CACHE_INT8, false>);
   return launched(launch_k(kern, dim3(splits, static_cast<unsigned>(units), 2), dim3(a.page * a.d / 32),
-                           2 * sizeof(int) * static_cast<size_t>(cap),
+                           few ? 0 : 2 * sizeof(int) * static_cast<size_t>(cap),
                            static_cast<cudaStream_t>(stream), a),
                   "cache_scatter_rows");
 }
@@ -514,11 +569,11 @@ extern "C" int focus_cache_load(const focus_cache* cache, const int32_t* table, 
   a.out[1] = reinterpret_cast<uint4*>(V);
   a.start = start;
   a.L = L;
-  const long long vecs = static_cast<long long>(L) << a.vec_shift, per = kLoadThreads * kLoadVecs;
+  const long long vecs = static_cast<long long>(L) << a.vec_shift;
+  const int per = kLoadThreads * kLoadVecs;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_load_kernel<FOCUS_CACHE_E4M3> : cache_load_kernel<FOCUS_CACHE_INT8>;
   return launched(launch_k(kern, dim3(static_cast<unsigned>((vecs + per - 1) / per), 2 * a.H, static_cast<unsigned>(units)),
-                           dim3(kLoadThreads), 0,
-                           static_cast<cudaStream_t>(stream), a),
+                           dim3(kLoadThreads), 0, static_cast<cudaStream_t>(stream), a),
                   "cache_load");
 }
 

@@ -388,7 +388,7 @@ class Pages:
 
 
 def _shape(t, want, name):
-    if tuple(t.shape) != tuple(want):
+    if t.shape != want:
         raise ValueError(f"{name} must be {tuple(want)}, got {tuple(t.shape)}")
 
 
@@ -396,12 +396,12 @@ def _cache_rows(X, Y, names, cache):
     """bf16 rows [n_mat, B, Hkv, n, d] (or without n_mat for one layer) that fit the cache -> (B, n)."""
     _need(X, torch.bfloat16, names[0])
     _need(Y, torch.bfloat16, names[1])
-    shape = X.shape if X.dim() == 5 else (1, *X.shape)
-    if len(shape) != 5 or (shape[0], shape[2], shape[4]) != (cache.n_mat, cache.Hkv, cache.d):
+    n_mat, B, Hkv, n, d = X.shape if X.dim() == 5 else (1, *X.shape) if X.dim() == 4 else (0, 0, 0, 0, 0)
+    if n_mat != cache.n_mat or Hkv != cache.Hkv or d != cache.d:
         raise ValueError(f"{names[0]} {tuple(X.shape)} does not fit a cache of {cache.n_mat} layers, {cache.Hkv} heads, "
                          f"d = {cache.d}")
     _shape(Y, X.shape, names[1])
-    return shape[1], shape[3]
+    return B, n
 
 
 def _table(table, B):
@@ -413,7 +413,8 @@ def _table(table, B):
 
 def _i32_list(t, n, name):
     _need(t, torch.int32, name, 1)
-    _shape(t, (n,), name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must be ({n},), got {tuple(t.shape)}")
 
 
 def focus_cache_store(K, V, cache, table, lens=None, stream=None):
