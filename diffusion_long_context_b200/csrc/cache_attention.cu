@@ -63,7 +63,7 @@ constexpr int kQParts = kSoftmaxWarps;   // warps that prepare the first queries
 constexpr int kMaxList = 1024;          // sinks, kept blocks
 constexpr int kDescs = 4;
 constexpr int kMasked = 1, kByKey = 2;
-constexpr int kLead = 2;                // places of a unit before its first tile (see unit_length)
+constexpr int kLead = 6;                // places of a unit before its first tile (see unit_length)
 
 struct CacheAttnArgs {
   const __nv_bfloat16* Q;
@@ -126,8 +126,10 @@ __device__ __forceinline__ Sequence sequence_of(const CacheAttnArgs& a, int b) {
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // Tiles lie on an axis on which every unit also takes kLead places before its first tile, for
-// what a run costs beyond its tiles (query rows, joining the groups, output): shares of equal
-// length then take about as long, whether they hold one long unit or many short ones.
+// what a run costs beyond its tiles (page lists, query rows, filling and draining the chain,
+// output): shares of equal length then take about as long, whether they hold one long unit or
+// many short ones. With 2, 4, 6 places: kept blocks at 32K 28.5, 28.0, 26.7 us, sixteen ragged
+// sequences 63, 57, 57 us, one sequence of 32K 64.5, 64.9, 64.6 us.
 __device__ __forceinline__ int unit_length(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
 
 // Length of the axis for one head slice of all sequences (a warp; the same in every lane).
@@ -737,6 +739,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.f = x.vm == 0.f || x.hi <= x.lo ? 0.f : x.vs / x.vm * prob_top<FMT>();
           x.part = __ballot_sync(0xffffffffu, x.lo > 0 || x.hi < a.page);
         };
+        auto find_sinks = [&]() {
+          // the sinks that no other slot holds: a sink is dropped inside the current
+          // block, inside a kept block, and when it was listed before
+          const int32_t* snk = a.sinks + (static_cast<size_t>(b) * a.Hkv + kvh) * a.S;
+          bool up = true;
+          int before = -1;
+          for (int i0 = 0; i0 < a.S; i0 += 32) {
+            const int v = i0 + lane < a.S ? snk[i0 + lane] : -1;
+            const int prev = __shfl_up_sync(0xffffffffu, v, 1);
+            const int pv = lane == 0 ? before : prev;
+            up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i0 + lane > 0);
+            if (i0 + lane < a.S) snk_s[i0 + lane] = v;
+            before = __shfl_sync(0xffffffffu, v, 31);
+          }
+          up = __all_sync(0xffffffffu, up);
+          __syncwarp();
+          for (int i0 = (a.S - 1) & ~31; i0 >= 0; i0 -= 32) {
+            const int i = i0 + lane, v = i < a.S ? snk_s[i] : -1;
+            bool drop = v < 0 || (v >= q.gs && v < q.ge);
+            if (!up)
+              for (int j = 0; j < i && !drop; ++j) drop = snk_s[j] == v;
+            if (!drop && v < q.P) {
+              const int col = v >> a.page_shift;
+              if (lists_sorted) {        // ascending, then -1
+                int lo = 0, hi = a.C;
+                while (lo < hi) {
+                  const int mid = (lo + hi) >> 1, x = blk_s[mid];
+                  if (x >= 0 && x < col) lo = mid + 1;
+                  else hi = mid;
+                }
+                drop = lo < a.C && blk_s[lo] == col;
+              } else {
+                for (int j = 0; j < a.C && !drop; ++j) drop = blk_s[j] == col;
+              }
+            }
+            __syncwarp();
+            if (drop && i < a.S) snk_s[i] = -1;
+            __syncwarp();
+          }
+          n_snk = a.S;
+        };
         if (SPARSE && lane == 0) {
           const long long g0 = a.g0[b];          // a current block that leaves the table
           if (g0 < 0 || g0 + a.G > static_cast<long long>(a.table_cols) * a.page) record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
@@ -830,60 +873,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vs[e] = on[e] ? v : 0.f;
               }
               {
-                if (n_snk < 0) {
-                  // the sinks that no other slot holds: a sink is dropped inside the current
-                  // block, inside a kept block, and when it was listed before
-                  const int32_t* snk = a.sinks + (static_cast<size_t>(b) * a.Hkv + kvh) * a.S;
-                  bool up = true;
-                  int before = -1;
-                  for (int i0 = 0; i0 < a.S; i0 += 32) {
-                    const int v = i0 + lane < a.S ? snk[i0 + lane] : -1;
-                    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-                    const int pv = lane == 0 ? before : prev;
-                    up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i0 + lane > 0);
-                    if (i0 + lane < a.S) snk_s[i0 + lane] = v;
-                    before = __shfl_sync(0xffffffffu, v, 31);
-                  }
-                  up = __all_sync(0xffffffffu, up);
-                  __syncwarp();
-                  for (int i0 = (a.S - 1) & ~31; i0 >= 0; i0 -= 32) {
-                    const int i = i0 + lane, v = i < a.S ? snk_s[i] : -1;
-                    bool drop = v < 0 || (v >= q.gs && v < q.ge);
-                    if (!up)
-                      for (int j = 0; j < i && !drop; ++j) drop = snk_s[j] == v;
-                    if (!drop && v < q.P) {
-                      const int col = v >> a.page_shift;
-                      if (lists_sorted) {        // ascending, then -1
-                        int lo = 0, hi = a.C;
-                        while (lo < hi) {
-                          const int mid = (lo + hi) >> 1, x = blk_s[mid];
-                          if (x >= 0 && x < col) lo = mid + 1;
-                          else hi = mid;
-                        }
-                        drop = lo < a.C && blk_s[lo] == col;
-                      } else {
-                        for (int j = 0; j < a.C && !drop; ++j) drop = blk_s[j] == col;
-                      }
-                    }
-                    __syncwarp();
-                    if (drop && i < a.S) snk_s[i] = -1;
-                    __syncwarp();
-                  }
-                  n_snk = a.S;
-                }
+                if (n_snk < 0) find_sinks();
+                // position, page, scales and rows of the four keys, step by step for all of them:
+                // each step is a round trip to memory
+                int pos[4], pg[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int i = k0 + e - q.n_pages * a.page;
-                  const int pos = i >= 0 && i < n_snk ? snk_s[i] : -1;
-                  if (pos < 0) continue;
-                  const int pg = checked_page(a.table, a.table_cols, b, pos >> a.page_shift, a.n_pages, a.dev_err);
-                  if (pg < 0) continue;
-                  const long long ph = static_cast<long long>(pg) * a.Hkv + kvh;
+                  pos[e] = i >= 0 && i < n_snk ? snk_s[i] : -1;
+                  pg[e] = -1;
+                  if (pos[e] >= 0 && (pos[e] >> a.page_shift) < a.table_cols) pg[e] = trow[pos[e] >> a.page_shift];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (pos[e] < 0) continue;
+                  if (pg[e] < 0 || pg[e] >= a.n_pages) {
+                    record_dev_error(a.dev_err, DEV_ERR_BAD_INDEX);
+                    pos[e] = -1;
+                    continue;
+                  }
+                  const long long ph = static_cast<long long>(pg[e]) * a.Hkv + kvh;
                   on[e] = true;
                   ks[e] = __ldg(a.scale[0] + ph);
                   vs[e] = __ldg(a.scale[1] + ph);
-                  const long long off = (ph * a.page + (pos & (a.page - 1))) * D;
-                  const uint32_t dk = smem_u32(smem) + sk * SM::kTile, dv = smem_u32(smem) + SM::kVRing + s * SM::kTile;
+                }
+                const uint32_t dk = smem_u32(smem) + sk * SM::kTile, dv = smem_u32(smem) + SM::kVRing + s * SM::kTile;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (pos[e] < 0) continue;
+                  const long long ph = static_cast<long long>(pg[e]) * a.Hkv + kvh;
+                  const long long off = (ph * a.page + (pos[e] & (a.page - 1))) * D;
 #pragma unroll
                   for (int c = 0; c < D / 16; ++c) {
                     cp_async16(dk + row_chunk<D>(4 * lane + e, c), a.code[0] + off + c * 16, 16);
