@@ -14,14 +14,13 @@
 //   S^T[key, q] = K_tile . Q^T        (M = 128 keys, N = queries, K = d)
 //   O^T[dim, q] = V_tile^T . P^T      (M = d,        N = queries, K = 128 keys)
 // hi and lo stand side by side in N, so a product of both is one MMA and their sums are added
-// when they are read (as two MMAs into one accumulator, which e4m3 could do, a tile took 1550
-// cycles of MMA instead of half that: at these widths an MMA costs about 100 cycles whatever
-// its N). V_tile^T is the row-major tile and P^T the rows of a key each, both MN-major.
+// when they are read (as two MMAs into one accumulator, which e4m3 could do, a tile took twice
+// the MMAs, and at these widths one costs about 55 cycles whatever its N). V_tile^T is the row-major tile and P^T the rows of a key each, both MN-major.
 //
 // Scales: a key's scale multiplies its row of S^T (a thread owns a key). A value's scale goes
-// into P, relative to the largest of the tile, and that largest into the sum of O over tiles,
-// which is kept in registers (a thread owns a dim): O^T of a tile is read back from tensor
-// memory and added with the factors that bring it to the running maximum.
+// into P, relative to the largest of the tile (so 2^-18 of a tile's largest p times value scale
+// is lost), and that largest into the sum of O over tiles, in fp32 in tensor memory: O^T of a
+// tile is read back and added with the factor from the tile's reference to the run's.
 //
 // Work is cut evenly: the 128-key tiles of all (sequence, KV head, slice of query rows) in a
 // row, gridDim.x contiguous shares of them, one CTA per SM. A share that begins or ends inside
@@ -29,20 +28,27 @@
 // writes zeros for the units without keys. So one long sequence among short ones still fills
 // the GPU, and a sequence's length is only read on the device.
 //
-// A tile goes through a chain of warps, each of which works on a tile of its own, so that four
-// tiles or more are under way and the latencies of the hand-overs (mbarriers, tensor memory,
-// shuffles: half of a tile's way) are covered by the other tiles:
+// Measured (graph replay): 32 heads of 32 rows over 32K keys 64 us, 4.2 TB/s of codes, and per
+// doubling of the keys 5.4 TB/s (of 6.5 that a copy reaches); 9.6 us of it are there with a
+// single tile: launch, page lookup, first bytes, the chain below, output, join. What bounds a
+// long sequence is how many tiles are under way: a tile takes 4 to 5 us through memory and the
+// chain, a CTA holds four of keys and six of values in 160 KB (a ring of seven, or five of keys,
+// gained nothing more), and every stage idles for a third of the time.
+//
+// A tile goes through a chain of warps, each of which works on a tile of its own, so that the
+// latencies of the hand-overs (mbarriers, tensor memory, shuffles: half of a tile's way) are
+// covered by the other tiles (cycles a tile in parentheses, of 1700 at 32 rows over 32K keys):
 //   16, 17  producers, a tile each in turn (TMA for pages, cp.async for sink rows)
-//   18      issues S^T = K Q^T, and sets the references (and owns tensor memory)
-//   0-3     the largest score of every column in each warp's 32 keys (and the query rows)
-//   4-11    two groups, a tile each in turn: exp, row sums, hi and lo of P
-//   19      issues O^T = V^T P^T
-//   12-15   sum of O^T over tiles; at the end of a unit, the output
+//   18      issues S^T = K Q^T (330), and sets the references (590); owns tensor memory
+//   0-3     the largest score of every column in each warp's 32 keys (760)
+//   4-11    two groups, a tile each in turn: exp, row sums, hi and lo of P (2600 a tile of two)
+//   19      issues O^T = V^T P^T (320)
+//   12-15   sum of O^T over tiles (790); at the end of a unit, the output
 // With one group taking a tile from its scores to its sum, and two such groups, a tile took 2200
-// cycles, most of them latency; the memory brings one every 1370. The loops over columns stay
-// short (16 columns, rolled, with what lasts from tile to tile in tensor memory instead of
-// registers): the stages run side by side on every scheduler, and unrolled over 32 columns their
-// code, together, left the instruction cache (3.2 of 13 warp cycles per instruction waited for one).
+// cycles, most of them latency. The loops over columns stay short (16 columns, rolled, with what
+// lasts from tile to tile in tensor memory instead of registers): the stages run side by side on
+// every scheduler, and unrolled over 32 columns their code, together, left the instruction cache
+// (3.2 of 13 warp cycles per instruction waited for one, 1.2 of 9.6 as it is).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -576,8 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kProducer && warp < kProducer + kProducers) {
     // ------------------------------------------------------------ producers
-    // Both walk over all runs; tile j of the CTA is producer j % 2's. (One alone, with about 1800
-    // cycles a tile for the copies' issue, the scales and the wait, was slower than the memory.)
+    // Both walk over all runs; tile j of the CTA is producer j % 2's: issuing the copies of a 32 KB
+    // tile takes 550 to 730 cycles, and with the scales and the wait one alone was slower than the
+    // memory.
     const int pw = warp - kProducer;
     int* const blk_s = bk->blk[pw];
     int* const snk_s = bk->snk[pw];

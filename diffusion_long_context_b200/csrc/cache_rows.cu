@@ -5,6 +5,11 @@
 // way round, a copy 1 and 1. The scale of a page needs the largest magnitude of its rows
 // before the first code can be written, so a group of threads holds a whole page of one head
 // in registers between the two: page * d / 32 threads with four 16-byte vectors each.
+//
+// Measured (graph replay, of 6.55 TB/s that a copy reaches): 268M elements in e4m3, pages of 64,
+// stored in 154 us (5.2 TB/s) and loaded in 157 us (5.1 TB/s), from memory's side bound by the
+// mix of reads and writes; 32 rows of 32 layers of 32 heads replaced in 16.5 us and read back in
+// 11.5 us, two rounds of CTAs of a few dependent loads each; a page copy 5.7 TB/s.
 #include <algorithm>
 
 #include "cache.cuh"
