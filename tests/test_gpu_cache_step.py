@@ -184,6 +184,35 @@ def test_scores_far_from_zero(F, fmt, score):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_a_page_that_is_not_finite_makes_its_readers_nan(F, fmt, bad, kv, sparse):
+    """One element of one head's keys or values is not finite: all rows of that head that read its
+    page are NaN, in every dim; the other head and a sequence that does not read the page are not."""
+    B, H, page, d, L = 2, 2, 32, 64, 300
+    w = World(F, fmt, 1, B, H, page, d, -(-L // page), seed=4)
+    K, V = rand_bf16((B, H, L, d), 1), rand_bf16((B, H, L, d), 2)
+    (K, V)[kv][0, 1, 70, 5] = bad
+    F.focus_cache_store(K, V, w.cache, w.t_table)
+    Q = rand_bf16((B, 4, 5, d), 6)
+    O = torch.full_like(Q, 5.0)
+    n_q = i32([5, 4])
+    if sparse:                                                  # the page through a sink and through a block
+        blocks = torch.tensor([[[0, -1], [2, 5]], [[2, -1], [2, 3]]], dtype=torch.int32, device=DEV)
+        sinks = torch.tensor([[[4], [10]], [[4], [70]]], dtype=torch.int32, device=DEV)
+        F.focus_cache_sparse_attention(Q, n_q, w.cache, w.t_table, i32([256, 256]), i32([256, 256]), 32, sinks, blocks, O)
+    else:
+        F.focus_cache_attention(Q, n_q, w.cache, w.t_table, i32([L, L]), O)
+    assert torch.all(torch.isnan(O[0, 2:]))
+    assert torch.all(torch.isfinite(O[0, :2])) and torch.all(torch.isfinite(O[1])) and not O[1, :, 4].any()
+    if sparse:
+        sinks[0, 1, 0], blocks[0, 1, 0] = 70, 7                 # by the sink alone
+        F.focus_cache_sparse_attention(Q, n_q, w.cache, w.t_table, i32([256, 256]), i32([256, 256]), 32, sinks, blocks, O)
+        assert torch.all(torch.isnan(O[0, 2:])) and torch.all(torch.isfinite(O[0, :2])) and torch.all(torch.isfinite(O[1]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_more_short_sequences_than_ctas(F, fmt):
     """Several runs to a CTA: 200 sequences, 2 KV heads, lengths about one tile, some empty."""
     B, H, page, d, qcap = 200, 2, 16, 64, 2
@@ -197,6 +226,51 @@ def test_more_short_sequences_than_ctas(F, fmt):
     n_q = rng.integers(0, qcap + 1, B)
     F.focus_cache_attention(Q, i32(n_q), w.cache, w.t_table, i32(lens), O)
     check_attention(w, Q, O, n_q, lambda b, h: np.arange(lens[b]), 1 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_inputs_that_change_from_call_to_call(F, graph):
+    """Lengths, row counts, prompt ends and table are written right before each call, without a wait
+    in between (the joining kernel reads some of them while the attention still runs)."""
+    B, H, page, d, qcap, n = 5, 2, 32, 128, 3, 24
+    rng = np.random.default_rng(9)
+    w = World(F, orc.E4M3, 1, B, H, page, d, 40, seed=3)
+    Q = rand_bf16((B, 4, qcap, d), 6)
+    lens, n_q = (i32(rng.integers(0, top, (n, B))) for top in (1281, qcap + 1))
+    P = i32(rng.integers(0, 1200, (n, B)))
+    tables = torch.stack([w.t_table[i32(rng.permutation(B)).long()] for _ in range(n)])
+    blocks = i32(rng.integers(-1, 38, (B, H, 6)))
+    ws = torch.empty(F.cache_workspace_bytes(B, 4, H, d, qcap), dtype=torch.uint8, device=DEV)
+    cur = [torch.zeros_like(x[0]) for x in (lens, n_q, P, tables)]
+    O = torch.zeros((n, 2, *Q.shape), dtype=torch.bfloat16, device=DEV)
+
+    def call(i, out, copy=True):
+        args = [x[i] for x in (lens, n_q, P, tables)]
+        if copy:
+            for c, x in zip(cur, args):
+                c.copy_(x)
+            args = cur
+        F.focus_cache_attention(Q, args[1], w.cache, args[3], args[0], out[0], ws=ws)
+        F.focus_cache_sparse_attention(Q, args[1], w.cache, args[3], args[2], args[2], 32, None, blocks, out[1], ws=ws)
+
+    if graph:
+        side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            for i in range(n):
+                call(i, O[i])
+        torch.cuda.current_stream().wait_stream(side)
+        g.replay()
+        g.replay()
+    else:
+        for i in range(n):
+            call(i, O[i])
+    torch.cuda.synchronize()
+    want = torch.zeros_like(O[0])
+    for i in range(n):
+        call(i, want, copy=False)
+        torch.cuda.synchronize()
+        assert torch.equal(O[i], want), i
 
 
 def test_lengths_below_zero_have_no_keys(F):
