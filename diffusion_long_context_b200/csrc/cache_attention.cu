@@ -668,14 +668,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t* blk = a.blocks + (static_cast<size_t>(b) * a.Hkv + kvh) * a.C;
           bool up = true;
           int before = -1;
-          for (int i0 = 0; i0 < a.C; i0 += 32) {
-            const int i = i0 + lane;
-            const int v = i < a.C ? blk[i] : -1;
-            const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-            const int pv = lane == 0 ? before : prev;
-            up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i > 0);
-            if (i < a.C) blk_s[i] = v;
-            before = __shfl_sync(0xffffffffu, v, 31);
+          for (int i0 = 0; i0 < a.C; i0 += 64) {
+            int vs[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) vs[u] = i0 + 32 * u + lane < a.C ? blk[i0 + 32 * u + lane] : -1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int i = i0 + 32 * u + lane, v = vs[u];
+              const int prev = __shfl_up_sync(0xffffffffu, v, 1);
+              const int pv = lane == 0 ? before : prev;
+              up = up && (v < 0 || v > pv) && !(v >= 0 && pv < 0 && i > 0);
+              if (i < a.C) blk_s[i] = v;
+              before = __shfl_sync(0xffffffffu, v, 31);
+            }
           }
           lists_sorted = __all_sync(0xffffffffu, up);
           __syncwarp();
@@ -1401,7 +1406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the units that several CTAs worked on (a warp per query row, a lane holds
-// D / 32 dims): weights 2^(m - M) over the parts' (m, l), 32 parts at a time. Units without
+// D / 32 dims): weights 2^(m - M) over the parts' (m, l), eight parts at a time. Units without
 // keys get zeros; units of one CTA are done already. Which parts there are follows from the
 // inputs alone, so it is worked out before the attention is done: two warps of 64 registers find
 // room beside an attention CTA. (All wait for it, those without work too: what follows in the
@@ -1438,36 +1443,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 16) cache_combine_kernel(cons
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   float l = 0.f, M = -INFINITY;
-  for (int c0 = s0; c0 <= s1; c0 += 32) {
-    const int c = c0 + lane;
+  // slot of share c's part: a share's last run is its part of a unit that goes on, its first of one
+  // that came before
+  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == s0 ? 1 : 0)) * NQ + n; };
+  constexpr int kAhead = 8;              // parts of O on their way together
+  for (int c0 = s0; c0 <= s1; c0 += kAhead) {
+    const int cn = min(kAhead, s1 - c0 + 1);
+    float v[kAhead][E];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float* src = a.part_o + slot(c0 + (i < cn ? i : 0)) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[i][0] = x.x, v[i][1] = x.y;
+      }
+    }
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (c <= s1) ml = a.part_ml[static_cast<size_t>(2 * c + (c == s0 ? 1 : 0)) * NQ + n];
+    if (lane < cn) ml = a.part_ml[slot(c0 + lane)];
     const float mn = max_nan(M, warp_max_nan(ml.x));
     const float back = l == 0.f ? 0.f : exp2_approx(M - mn);
     const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - mn);
     float lw = f * ml.y;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
-    l = l * back + lw;
+    for (int off = kAhead / 2; off; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+    l = l * back + __shfl_sync(0xffffffffu, lw, 0);
     M = mn;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= back;
-    const int cn = min(32, s1 - c0 + 1);
-#pragma unroll 8
-    for (int i = 0; i < cn; ++i) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* src = a.part_o + (static_cast<size_t>(2 * (c0 + i) + (c0 + i == s0 ? 1 : 0)) * NQ + n) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        o[0] += fi * v.x;
-        o[1] += fi * v.y;
-        o[2] += fi * v.z;
-        o[3] += fi * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        o[0] += fi * v.x;
-        o[1] += fi * v.y;
-      }
+      if (i < cn)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += fi * v[i][e];
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
