@@ -321,8 +321,8 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// Waits for phase `parity` (a whole warp). The thread sleeps in the barrier for as long as the
-// hint says (a wait that polls takes issue slots from the warps that have work); false when the
+// Waits for phase `parity` (a whole warp), in the barrier as long as the hardware suspends the
+// thread (a wait that polls takes issue slots from the warps that have work); false when the
 // limit runs out or another warp gave up.
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

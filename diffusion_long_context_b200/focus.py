@@ -104,9 +104,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:                   # (torch.cuda.current_stream() builds an object: 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream
 
 
@@ -334,11 +334,12 @@ CACHE_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
 def _here(name, *tensors):
-    """The tensors of a call lie on the current device (whose stream and error word it uses)."""
+    """The tensors of a call lie on the current device (whose stream and error word it uses); its index."""
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{name}: tensor on {t.device}, the current device is cuda:{cur}")
+    return cur
 
 
 class Cache:
@@ -423,8 +424,8 @@ def focus_cache_store(K, V, cache, table, lens=None, stream=None):
     cols = _table(table, B)
     if lens is not None:
         _i32_list(lens, B, "lens")
-    _here("focus_cache_store", K, V, cache.k, table, lens)
-    st = lib.focus_cache_store(_ptr(K), _ptr(V), B, L, _ptr(lens), _ptr(table), cols, cache._ref, _stream(stream))
+    cur = _here("focus_cache_store", K, V, cache.k, table, lens)
+    st = lib.focus_cache_store(_ptr(K), _ptr(V), B, L, _ptr(lens), _ptr(table), cols, cache._ref, _stream(stream, cur))
     _check(st, "focus_cache_store")
 
 
@@ -437,9 +438,9 @@ def focus_cache_scatter_rows(K_rows, V_rows, rows, n_rows, cache, table, lens, s
     _i32_list(n_rows, B, "n_rows")
     _i32_list(lens, B, "lens")
     cols = _table(table, B)
-    _here("focus_cache_scatter_rows", K_rows, V_rows, rows, n_rows, cache.k, table, lens)
+    cur = _here("focus_cache_scatter_rows", K_rows, V_rows, rows, n_rows, cache.k, table, lens)
     st = lib.focus_cache_scatter_rows(_ptr(K_rows), _ptr(V_rows), _ptr(rows), _ptr(n_rows), B, cap, _ptr(lens),
-                                      _ptr(table), cols, cache._ref, _stream(stream))
+                                      _ptr(table), cols, cache._ref, _stream(stream, cur))
     _check(st, "focus_cache_scatter_rows")
 
 
@@ -448,9 +449,9 @@ def focus_cache_load(cache, table, lens, start, K, V, stream=None):
     B, L = _cache_rows(K, V, ("K", "V"), cache)
     _i32_list(lens, B, "lens")
     cols = _table(table, B)
-    _here("focus_cache_load", K, V, cache.k, table, lens)
+    cur = _here("focus_cache_load", K, V, cache.k, table, lens)
     st = lib.focus_cache_load(cache._ref, _ptr(table), cols, _ptr(lens), B, start, L, _ptr(K), _ptr(V),
-                              _stream(stream))
+                              _stream(stream, cur))
     _check(st, "focus_cache_load")
 
 
@@ -476,10 +477,10 @@ def focus_cache_attention(Q, n_q, cache, table, lens, O, scale=None, ws=None, st
     B, Hq, qcap, d, ws, ws_bytes = _cache_queries(Q, n_q, cache, O, ws)
     _i32_list(lens, B, "lens")
     cols = _table(table, B)
-    _here("focus_cache_attention", Q, n_q, cache.k, table, lens, O, ws)
+    cur = _here("focus_cache_attention", Q, n_q, cache.k, table, lens, O, ws)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     st = lib.focus_cache_attention(_ptr(Q), _ptr(n_q), cache._ref, _ptr(table), cols, _ptr(lens), B, Hq, qcap,
-                                   float(scale), _ptr(O), _ptr(ws), ws_bytes, _stream(stream))
+                                   float(scale), _ptr(O), _ptr(ws), ws_bytes, _stream(stream, cur))
     _check(st, "focus_cache_attention")
 
 
@@ -499,11 +500,11 @@ def focus_cache_sparse_attention(Q_active, n_active, cache, table, P, g0, G, sin
         S = sinks.shape[2]
         _shape(sinks, (B, cache.Hkv, S), "sinks")
     cols = _table(table, B)
-    _here("focus_cache_sparse_attention", Q_active, n_active, cache.k, table, P, g0, sinks, blocks, O_active, ws)
+    cur = _here("focus_cache_sparse_attention", Q_active, n_active, cache.k, table, P, g0, sinks, blocks, O_active, ws)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     st = lib.focus_cache_sparse_attention(_ptr(Q_active), _ptr(n_active), cache._ref, _ptr(table), cols, _ptr(P),
                                           _ptr(g0), G, _ptr(sinks), S, _ptr(blocks), C, B, Hq, qcap, float(scale),
-                                          _ptr(O_active), _ptr(ws), ws_bytes, _stream(stream))
+                                          _ptr(O_active), _ptr(ws), ws_bytes, _stream(stream, cur))
     _check(st, "focus_cache_sparse_attention")
 
 
@@ -513,8 +514,8 @@ def focus_pages_reserve(pages, seqs, want, status, stream=None):
     n = seqs.shape[0]
     _i32_list(want, n, "want")
     _i32_list(status, 1, "status")
-    _here("focus_pages_reserve", pages.refs, seqs, want, status)
-    st = lib.focus_pages_reserve(pages._ref, _ptr(seqs), _ptr(want), n, _ptr(status), _stream(stream))
+    cur = _here("focus_pages_reserve", pages.refs, seqs, want, status)
+    st = lib.focus_pages_reserve(pages._ref, _ptr(seqs), _ptr(want), n, _ptr(status), _stream(stream, cur))
     _check(st, "focus_pages_reserve")
 
 
@@ -524,8 +525,8 @@ def focus_pages_fork(pages, src, dst, keep, stream=None):
     n = src.shape[0]
     _i32_list(dst, n, "dst")
     _i32_list(keep, n, "keep")
-    _here("focus_pages_fork", pages.refs, src, dst, keep)
-    st = lib.focus_pages_fork(pages._ref, _ptr(src), _ptr(dst), _ptr(keep), n, _stream(stream))
+    cur = _here("focus_pages_fork", pages.refs, src, dst, keep)
+    st = lib.focus_pages_fork(pages._ref, _ptr(src), _ptr(dst), _ptr(keep), n, _stream(stream, cur))
     _check(st, "focus_pages_fork")
 
 
@@ -545,9 +546,9 @@ def focus_pages_own(pages, seqs, first, last, pairs, n_pairs, status, stream=Non
     _i32_list(last, n, "last")
     _i32_list(status, 1, "status")
     cap = _pairs(pairs, n_pairs)
-    _here("focus_pages_own", pages.refs, seqs, first, last, pairs, n_pairs, status)
+    cur = _here("focus_pages_own", pages.refs, seqs, first, last, pairs, n_pairs, status)
     st = lib.focus_pages_own(pages._ref, _ptr(seqs), _ptr(first), _ptr(last), n, _ptr(pairs), cap, _ptr(n_pairs),
-                             _ptr(status), _stream(stream))
+                             _ptr(status), _stream(stream, cur))
     _check(st, "focus_pages_own")
 
 
@@ -556,8 +557,8 @@ def focus_pages_release(pages, seqs, keep, stream=None):
     _need(seqs, torch.int32, "seqs", 1)
     n = seqs.shape[0]
     _i32_list(keep, n, "keep")
-    _here("focus_pages_release", pages.refs, seqs, keep)
-    st = lib.focus_pages_release(pages._ref, _ptr(seqs), _ptr(keep), n, _stream(stream))
+    cur = _here("focus_pages_release", pages.refs, seqs, keep)
+    st = lib.focus_pages_release(pages._ref, _ptr(seqs), _ptr(keep), n, _stream(stream, cur))
     _check(st, "focus_pages_release")
 
 
@@ -566,14 +567,14 @@ def focus_pages_compact(pages, pairs, n_pairs, remap, stream=None):
     copy, remap [n_pages] = each page's new index (-1: free)."""
     cap = _pairs(pairs, n_pairs)
     _i32_list(remap, pages.n_pages, "remap")
-    _here("focus_pages_compact", pages.refs, pairs, n_pairs, remap)
-    st = lib.focus_pages_compact(pages._ref, _ptr(pairs), cap, _ptr(n_pairs), _ptr(remap), _stream(stream))
+    cur = _here("focus_pages_compact", pages.refs, pairs, n_pairs, remap)
+    st = lib.focus_pages_compact(pages._ref, _ptr(pairs), cap, _ptr(n_pairs), _ptr(remap), _stream(stream, cur))
     _check(st, "focus_pages_compact")
 
 
 def focus_pages_copy(cache, pairs, n_pairs, stream=None):
     """Codes and scales of page pairs[r, 0] to page pairs[r, 1] in every layer, r < n_pairs[0]."""
     cap = _pairs(pairs, n_pairs)
-    _here("focus_pages_copy", cache.k, pairs, n_pairs)
-    st = lib.focus_pages_copy(cache._ref, _ptr(pairs), _ptr(n_pairs), cap, _stream(stream))
+    cur = _here("focus_pages_copy", cache.k, pairs, n_pairs)
+    st = lib.focus_pages_copy(cache._ref, _ptr(pairs), _ptr(n_pairs), cap, _stream(stream, cur))
     _check(st, "focus_pages_copy")

@@ -62,7 +62,6 @@ def test_step_from_the_cache(F, fmt, variant):
     if variant != "plain":
         cfg = cfg.replace(dense_tail=1, relevance="focus", sink_agg="mean_query")
     step, plain = make_steps(cfg, fmt)
-    w = World.__new__(World)
     for l in range(cfg.n_layers):                        # block entry stored every layer
         for kv, X in enumerate((step.K[l], step.V[l])):
             got = (step.cache.k, step.cache.v)[kv][l:l + 1].view(torch.uint8).cpu().numpy()
