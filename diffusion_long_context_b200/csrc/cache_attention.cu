@@ -399,6 +399,21 @@ __device__ __forceinline__ void split4(float2 p01, float2 p23, uint32_t& hi, uin
   }
 }
 
+// Two scores of a key: the products times its scale, -infinity if it is masked. In int8 the
+// products are finite whatever the codes, so that is an addend (a multiply-add instead of a
+// multiply and two selects: 224 rows over 16K keys 36.9 -> 35.5 us); in e4m3 a masked key's may
+// be NaN.
+template <int FMT>
+__device__ __forceinline__ float2 key_score(float2 s, float scale, bool off) {
+  if constexpr (FMT == FOCUS_CACHE_INT8) {
+    const float k = off ? 0.f : scale, add = off ? -INFINITY : 0.f;
+    return fma2(s, make_float2(k, k), make_float2(add, add));
+  } else {
+    const float2 x = mul2(s, make_float2(scale, scale));
+    return off ? make_float2(-INFINITY, -INFINITY) : x;
+  }
+}
+
 // The product of hi and lo from their accumulators.
 template <int FMT>
 __device__ __forceinline__ float both(uint32_t hi, uint32_t lo) {
@@ -1185,9 +1200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int n = 0; n < 16; n += 4) {
-              float2 x0 = mul2(both2<FMT>(r + n, r2 + n), make_float2(ks, ks));
-              float2 x1 = mul2(both2<FMT>(r + n + 2, r2 + n + 2), make_float2(ks, ks));
-              if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
+              const float2 x0 = key_score<FMT>(both2<FMT>(r + n, r2 + n), ks, off);
+              const float2 x1 = key_score<FMT>(both2<FMT>(r + n + 2, r2 + n + 2), ks, off);
               float4 m;
               m.x = warp_max_nan(x0.x);
               m.y = warp_max_nan(x0.y);
@@ -1263,9 +1277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float2 x0 = mul2(both2<FMT>(r + 4 * i, r2 + 4 * i), make_float2(key.x, key.x));
-              float2 x1 = mul2(both2<FMT>(r + 4 * i + 2, r2 + 4 * i + 2), make_float2(key.x, key.x));
-              if (off) x0 = x1 = make_float2(-INFINITY, -INFINITY);
+              const float2 x0 = key_score<FMT>(both2<FMT>(r + 4 * i, r2 + 4 * i), key.x, off);
+              const float2 x1 = key_score<FMT>(both2<FMT>(r + 4 * i + 2, r2 + 4 * i + 2), key.x, off);
               const float4 rv = *reinterpret_cast<const float4*>(&bk->ref[e][h + 4 * i]);
               const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[e][h + 4 * i]);
               const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[we][h + 4 * i]);
