@@ -40,6 +40,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
   return unpair(r);
 }
+// a b rounded to fp32, whatever is added to it: ptxas 12.9 makes one multiply-add of a packed
+// product and a sum (mul2 and add2, each with its .rn), which rounds once, at the end.
+__device__ __forceinline__ float2 round2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 
 template <int FMT>
 struct CodeTop {

@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float ref = 0.f;                       // (a tile without keys adds nothing)
           uint32_t be16 = 0;                     // bf16 of the factor
           if (mt != -INFINITY) {
-            ref = ceilf(mt * qs);
+            ref = ceilf(__fmul_rn(mt, qs));
             if (ref > m_ref + 30.f || m_ref == -INFINITY) m_ref = ref;
             const float e = ref - m_ref;         // a whole number
             be16 = e != e ? 0x7fc0u : e < -126.f ? 0u : static_cast<uint32_t>(127 + static_cast<int>(e)) << 7;
@@ -1282,8 +1282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 rv = *reinterpret_cast<const float4*>(&bk->ref[e][h + 4 * i]);
               const uint2 bv = *reinterpret_cast<const uint2*>(&bk->be[e][h + 4 * i]);
               const float4 qv = *reinterpret_cast<const float4*>(&bk->qs[we][h + 4 * i]);
-              float2 p0 = fma2(x0, make_float2(qv.x, qv.y), make_float2(rv.x, rv.y));
-              float2 p1 = fma2(x1, make_float2(qv.z, qv.w), make_float2(rv.z, rv.w));
+              // (The product is rounded before the reference is taken off, as that which gave the
+              // reference was, so p <= 1 however large the scores. By one multiply-add, whose product
+              // is exact, p came out above 1 where the reference's had been rounded down, and left the
+              // 8 bits of a part.)
+              float2 p0 = add2(round2(x0, make_float2(qv.x, qv.y)), make_float2(rv.x, rv.y));
+              float2 p1 = add2(round2(x1, make_float2(qv.z, qv.w)), make_float2(rv.z, rv.w));
               p0 = make_float2(exp2_approx(p0.x), exp2_approx(p0.y));
               p1 = make_float2(exp2_approx(p1.x), exp2_approx(p1.y));
               const float2 l0 = fma2(p0, bf16_pair(bv.x), make_float2(__uint_as_float(rl[4 * i]), __uint_as_float(rl[4 * i + 1])));

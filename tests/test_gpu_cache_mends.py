@@ -1,0 +1,43 @@
+"""Calls of the 8-bit cache at the ends of their ranges: scores of any size, keys that each show in
+the output, workspaces of other streams, pages that run short over several passes."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as orc
+from test_gpu_cache import DEV, DTYPE, F, FMTS, World, i32, no_device_error, rand_bf16  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("score", [1e3, 1e5, -1e5, 1e6, 1e7, -1e7, 3e8, 1e12, 1e30])
+def test_keys_that_take_all_the_weight(F, fmt, score):
+    """Three keys of 300, two of them in one tile, share the largest score, and every other lies far
+    below: the output is the mean of their values, however large the scores.
+
+    256 heads of 6 rows, each with a size of its own between one and four times `score`. A row's
+    elements are alike and the codes powers of two, so both enter in 8 + 8 bits without a rounding and
+    the three scores are equal in fp32 as well. Each of their probabilities may be off by 2^-8 of
+    itself (2^-14 in int8), the output by half a step, 2^-8."""
+    H, page, d, L = 256, 16, 64, 300
+    rng = np.random.default_rng(7)
+    w = World(F, fmt, 1, 1, H, page, d, -(-L // page), seed=5)
+    code = lambda x: orc.nearest_codes(np.float32([x]), fmt)[0]
+    best = [17, 100, 290]
+    w.codes[0][:] = code(32.0 if score > 0 else 127.0)       # (below, or with a negative sign far above)
+    for pos in best:
+        w.codes[0][0, w.table[0, pos // page], :, pos % page] = code(64.0)
+    w.scales[0][:] = ((1 + rng.random(H)) / 64).astype(np.float32)
+    w.scales[1][:] = np.float32(1 / orc.TOP[fmt])
+    w.upload(F)
+    q = torch.from_numpy((1 + rng.random((1, 2 * H, 3, 1))).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    Q = q.expand(-1, -1, -1, d).contiguous()
+    O = torch.zeros_like(Q)
+    F.focus_cache_attention(Q, None, w.cache, w.t_table, i32([L]), O, scale=score / d)
+    for h in range(H):
+        V = orc.values(w.codes[1], w.scales[1], w.table[0], best, h, fmt)
+        err = np.abs(O[0, 2 * h:2 * h + 2].double().cpu().numpy() - V.mean(axis=0))
+        lim = 2.0 ** -8 * (np.abs(V.mean(axis=0)) + np.abs(V).mean(axis=0))
+        assert np.all(err <= lim), (h, float((err / lim).max()))
