@@ -196,14 +196,19 @@ def sparse_workspace_bytes(B, Hq, Hkv, L, d, acap, S, C, bs, P, g0, g1):
     return int(lib.focus_sparse_workspace_bytes(B, Hq, Hkv, L, d, acap, S, C, bs, P, g0, g1))
 
 
-def _workspace(nbytes, device, ws):
+def _workspace(nbytes, device, ws, stream=None):
+    """The caller's workspace, or one that lives as long as the call's binding. That one is taken from
+    the memory of the stream that the kernels run on: only there is what comes after ordered behind them."""
     if nbytes == 0:
         return None, 0
     if ws is not None:
         if ws.numel() * ws.element_size() < nbytes:
             raise ValueError(f"workspace needs {nbytes} bytes")
         return ws, ws.numel() * ws.element_size()
-    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
 def focus_dense_attention(Q, n_q, K, V, O, scale=None, colsum=None, ws=None, stream=None):
@@ -219,7 +224,7 @@ def focus_dense_attention(Q, n_q, K, V, O, scale=None, colsum=None, ws=None, str
     Hkv, L = K.shape[1], K.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     need = dense_workspace_bytes(B, Hq, Hkv, L, d, qcap, colsum is not None)
-    ws, ws_bytes = _workspace(need, Q.device, ws)
+    ws, ws_bytes = _workspace(need, Q.device, ws, stream)
     st = lib.focus_dense_attention(_ptr(Q), _ptr(n_q), _ptr(K), _ptr(V), B, Hq, Hkv, L, d, qcap, float(scale),
                                    _ptr(O), _ptr(colsum), _ptr(ws), ws_bytes, _stream(stream))
     _check(st, "focus_dense_attention")
@@ -239,7 +244,7 @@ def focus_dense_attention_sinks(Q, n_q, K, V, O, colsum, sinks, scale=None, ws=N
     Hkv, L = K.shape[1], K.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     need = dense_workspace_bytes(B, Hq, Hkv, L, d, qcap, True)
-    ws, ws_bytes = _workspace(need, Q.device, ws)
+    ws, ws_bytes = _workspace(need, Q.device, ws, stream)
     st = lib.focus_dense_attention_sinks(_ptr(Q), _ptr(n_q), _ptr(K), _ptr(V), B, Hq, Hkv, L, d, qcap, float(scale),
                                          _ptr(O), _ptr(colsum), sinks.shape[2], _ptr(sinks), _ptr(ws), ws_bytes,
                                          _stream(stream))
@@ -258,7 +263,7 @@ def focus_full_refresh(Q, K, V, O, P, bs, kbar, scale=None, ws=None, stream=None
     Hkv = K.shape[1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     need = dense_workspace_bytes(B, Hq, Hkv, L, d, L, False)
-    ws, ws_bytes = _workspace(need, Q.device, ws)
+    ws, ws_bytes = _workspace(need, Q.device, ws, stream)
     st = lib.focus_full_refresh(_ptr(Q), _ptr(K), _ptr(V), B, Hq, Hkv, L, d, float(scale), _ptr(O), P, bs, _ptr(kbar),
                                 _ptr(ws), ws_bytes, _stream(stream))
     _check(st, "focus_full_refresh")
@@ -288,7 +293,7 @@ def focus_sparse_attention(Q_active, n_active, K, V, sinks, blocks, bs, P, g0, g
     C = blocks.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     need = sparse_workspace_bytes(B, Hq, Hkv, L, d, acap, S, C, bs, P, g0, g1)
-    ws, ws_bytes = _workspace(need, Q_active.device, ws)
+    ws, ws_bytes = _workspace(need, Q_active.device, ws, stream)
     st = lib.focus_sparse_attention(_ptr(Q_active), _ptr(n_active), _ptr(K), _ptr(V), _ptr(sinks), S,
                                     _ptr(blocks), C, bs, P, g0, g1, B, Hq, Hkv, L, d, acap, float(scale),
                                     _ptr(O_active), _ptr(ws), ws_bytes, _stream(stream))
@@ -313,7 +318,7 @@ def focus_sparse_attention_fused(Q_active, n_active, K, V, kbar, C, sinks, bs, P
     S = 0 if sinks is None else sinks.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     need = sparse_workspace_bytes(B, Hq, Hkv, L, d, acap, S, C, bs, P, g0, g1)
-    ws, ws_bytes = _workspace(need, Q_active.device, ws)
+    ws, ws_bytes = _workspace(need, Q_active.device, ws, stream)
     st = lib.focus_sparse_attention_fused(_ptr(Q_active), _ptr(n_active), _ptr(K), _ptr(V), _ptr(kbar), nb, C,
                                           _ptr(sinks), S, bs, P, g0, g1, B, Hq, Hkv, L, d, acap, float(scale),
                                           _ptr(blocks), _ptr(O_active), _ptr(ws), ws_bytes, _stream(stream))
@@ -459,7 +464,7 @@ def cache_workspace_bytes(B, Hq, Hkv, d, qcap):
     return int(lib.focus_cache_workspace_bytes(B, Hq, Hkv, d, qcap))
 
 
-def _cache_queries(Q, n_q, cache, O, ws):
+def _cache_queries(Q, n_q, cache, O, ws, stream):
     _need(Q, torch.bfloat16, "Q", 4)
     _need(O, torch.bfloat16, "O", 4)
     B, Hq, qcap, d = Q.shape
@@ -468,13 +473,13 @@ def _cache_queries(Q, n_q, cache, O, ws):
     _shape(O, Q.shape, "O")
     if n_q is not None:
         _i32_list(n_q, B, "n_q")
-    ws, ws_bytes = _workspace(cache_workspace_bytes(B, Hq, cache.Hkv, d, qcap), Q.device, ws)
+    ws, ws_bytes = _workspace(cache_workspace_bytes(B, Hq, cache.Hkv, d, qcap), Q.device, ws, stream)
     return B, Hq, qcap, d, ws, ws_bytes
 
 
 def focus_cache_attention(Q, n_q, cache, table, lens, O, scale=None, ws=None, stream=None):
     """Dense attention of Q [B, Hq, qcap, d] over positions [0, lens[b]) of a one-layer cache."""
-    B, Hq, qcap, d, ws, ws_bytes = _cache_queries(Q, n_q, cache, O, ws)
+    B, Hq, qcap, d, ws, ws_bytes = _cache_queries(Q, n_q, cache, O, ws, stream)
     _i32_list(lens, B, "lens")
     cols = _table(table, B)
     cur = _here("focus_cache_attention", Q, n_q, cache.k, table, lens, O, ws)
@@ -488,7 +493,7 @@ def focus_cache_sparse_attention(Q_active, n_active, cache, table, P, g0, G, sin
                                  ws=None, stream=None):
     """Sparse attention from a one-layer cache over sinks U kept blocks (of a page each) U [g0, g0 + G);
     P, g0 [B] int32, sinks [B, Hkv, S] or None, blocks [B, Hkv, C]."""
-    B, Hq, qcap, d, ws, ws_bytes = _cache_queries(Q_active, n_active, cache, O_active, ws)
+    B, Hq, qcap, d, ws, ws_bytes = _cache_queries(Q_active, n_active, cache, O_active, ws, stream)
     _i32_list(P, B, "P")
     _i32_list(g0, B, "g0")
     _need(blocks, torch.int32, "blocks", 3)

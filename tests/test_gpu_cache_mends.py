@@ -41,3 +41,31 @@ def test_keys_that_take_all_the_weight(F, fmt, score):
         err = np.abs(O[0, 2 * h:2 * h + 2].double().cpu().numpy() - V.mean(axis=0))
         lim = 2.0 ** -8 * (np.abs(V.mean(axis=0)) + np.abs(V).mean(axis=0))
         assert np.all(err <= lim), (h, float((err / lim).max()))
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.parametrize("sparse", [False, True])
+def test_a_call_on_a_given_stream_takes_its_workspace_there(F, sparse):
+    """The side stream is behind, so its call has not started when the current stream fills memory of
+    the workspace's size: neither may write into the other's."""
+    w = World(F, orc.E4M3, 1, 1, 2, 64, 128, 40, seed=3)
+    Q = rand_bf16((1, 4, 16, 128), 4)
+    lens, P, blocks = i32([2500]), i32([2400]), i32([[list(range(30)), list(range(5, 35))]])
+    side = torch.cuda.Stream()
+
+    def call(O, **kw):
+        if sparse:
+            F.focus_cache_sparse_attention(Q, None, w.cache, w.t_table, P, P, 64, None, blocks, O, **kw)
+        else:
+            F.focus_cache_attention(Q, None, w.cache, w.t_table, lens, O, **kw)
+
+    want, O = torch.zeros_like(Q), torch.zeros_like(Q)
+    call(want)
+    n = F.cache_workspace_bytes(1, 4, 2, 128, 16)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    call(O, stream=side)
+    taken = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in taken) and torch.equal(O, want)
