@@ -275,29 +275,28 @@ __global__ void __launch_bounds__(kPageThreads) pages_own_kernel(const PageArgs 
   if (i < a.n) s_pre[i] = pre;
   if (i == 0) s_pre[a.n] = entries;
   __syncthreads();
+  // Entry e of the listed ranges: its page (-1: none, or listed before) and its place in the table.
+  auto entry = [&](int e, int& slot, bool report) {
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pre[mid] <= e) lo = mid;
+      else hi = mid - 1;
+    }
+    const int j = s_first[lo] + (e - s_pre[lo]);
+    for (int o = 0; o < lo; ++o)
+      if (s_seq[o] == s_seq[lo] && j >= s_first[o] && j < s_last[o]) return -1;
+    slot = s_seq[lo] * a.cols + j;
+    const int x = a.table[slot];
+    if (x >= 0 && x < a.n_pages) return x;
+    if (report) flag(a);
+    return -1;
+  };
   int found = 0;                         // copies needed so far (the same in every thread)
   for (int e0 = 0; e0 < entries; e0 += kPageThreads) {
     const int e = e0 + i;
-    int x = -1, slot = -1;
-    if (e < entries) {
-      int lo = 0, hi = a.n - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_pre[mid] <= e) lo = mid;
-        else hi = mid - 1;
-      }
-      const int j = s_first[lo] + (e - s_pre[lo]);
-      bool again = false;                // the same entry of the table was listed before
-      for (int o = 0; o < lo; ++o) again |= s_seq[o] == s_seq[lo] && j >= s_first[o] && j < s_last[o];
-      if (!again) {
-        slot = s_seq[lo] * a.cols + j;
-        x = a.table[slot];
-        if (x < 0 || x >= a.n_pages) {
-          flag(a);
-          x = -1;
-        }
-      }
-    }
+    int slot = -1;
+    const int x = e < entries ? entry(e, slot, true) : -1;
     s_x[i] = x;
     __syncthreads();
     bool copies = false;
@@ -321,6 +320,23 @@ __global__ void __launch_bounds__(kPageThreads) pages_own_kernel(const PageArgs 
   __syncthreads();
   if (found > room) {
     for (int r = i; r < min(found, a.pair_cap); r += kPageThreads) atomicAdd(&a.refs[a.pairs[2 * r]], 1);
+    if (found > a.pair_cap) {
+      // Copies without a pair have not lowered their page's count, so what came after them was
+      // counted too high. Counted anew: all m entries of a page are taken off its count R and put
+      // back one by one; min(m, R - 1) of them, the copies, find another one there.
+      __syncthreads();
+      int slot = -1, copies = 0;
+      for (int e = i; e < entries; e += kPageThreads) {
+        const int x = entry(e, slot, false);
+        if (x >= 0) atomicSub(&a.refs[x], 1);
+      }
+      __syncthreads();
+      for (int e = i; e < entries; e += kPageThreads) {
+        const int x = entry(e, slot, false);
+        if (x >= 0 && atomicAdd(&a.refs[x], 1) >= 1) ++copies;
+      }
+      block_scan(copies, s_warp, &found);
+    }
     if (i == 0) {
       *a.status = found - room;
       *a.n_pairs = 0;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import cache_oracle as orc
-from test_gpu_cache import DEV, DTYPE, F, FMTS, World, i32, no_device_error, rand_bf16  # noqa: F401
+from test_gpu_cache import DEV, DTYPE, F, FMTS, PageWorld, World, i32, no_device_error, rand_bf16  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,33 @@ def test_a_call_on_a_given_stream_takes_its_workspace_there(F, sparse):
     taken = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for _ in range(8)]
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in taken) and torch.equal(O, want)
+
+
+# ------------------------------------------------------------------ pages
+@pytest.mark.parametrize("cap", [0, 1, 100, 1500, 2500, 2799, 2800])
+@pytest.mark.parametrize("keeps", [[400] * 7, [400, 399, 7, 1, 0, 400, 350]])
+def test_own_says_how_many_are_missing(F, cap, keeps):
+    """Eight sequences with up to 400 shared pages, more entries than one pass takes, and room for `cap`
+    pairs: the number that is missing, and nothing changed; then, with room, what has to be copied."""
+    w = PageWorld(F, 4000, 9, 400)
+    w.reserve([0], [400])
+    w.fork([0] * 7, list(range(1, 8)), keeps)
+    order = [3, 0, 5, 1, 7, 2, 6, 4]
+    for seqs, first, last in ((order, [0] * 8, [400] * 8), (order + [0, 7], [3] * 8 + [0, 0], [390] * 8 + [400, 400])):
+        short = w.o.own(seqs, first, last, 0)[0]              # (copies that are needed; changes nothing)
+        F.focus_pages_own(w.p, i32(seqs), i32(first), i32(last), w.pairs[:cap], w.n_pairs, w.status)
+        want, pairs = w.o.own(seqs, first, last, cap)
+        assert want == max(0, short - cap)
+        assert int(w.status) == want and w.got_pairs() == pairs
+        w.same()
+
+
+def test_own_is_short_of_pages_and_of_pairs(F):
+    """Fewer free pages than pairs, and the other way: the smaller room counts."""
+    w = PageWorld(F, 700, 5, 300)
+    w.reserve([0], [300])
+    w.fork([0] * 4, [1, 2, 3, 4], [300] * 4)                  # 1200 copies for 400 free pages
+    for cap in (700, 400, 399, 20):
+        F.focus_pages_own(w.p, i32([0, 1, 2, 3, 4]), i32([0] * 5), i32([300] * 5), w.pairs[:cap], w.n_pairs, w.status)
+        assert int(w.status) == 1200 - min(cap, 400) and int(w.n_pairs) == 0
+        w.same()
