@@ -5,6 +5,7 @@
 
 #include <cuda_fp8.h>
 
+#include "cache_index.cuh"
 #include "focus_common.cuh"
 
 namespace focus {

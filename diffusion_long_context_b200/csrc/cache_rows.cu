@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(512) cache_store_kernel(const RowArgs a) {
   const int t = threadIdx.x & (gt - 1);
   const int mat = blockIdx.z / a.B, b = blockIdx.z - mat * a.B;
   const int j = blockIdx.x * (blockDim.x >> gshift) + (threadIdx.x >> gshift);   // page of the sequence
-  const int rows = j < a.cols ? min(a.page, (a.lens ? max(0, min(a.lens[b], a.L)) : a.L) - (j << a.page_shift)) : 0;
-  const int n = rows << a.vec_shift;                    // vectors that are stored (none if negative)
+  const int len = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
+  const int n = j < a.cols ? stored_vectors(len, j, a.page_shift, a.vec_shift) : 0;
   const long long mbh = static_cast<long long>(blockIdx.z) * a.H + h;
   const uint4* src = a.X[kv] + ((mbh * a.L + (static_cast<long long>(j) << a.page_shift)) << a.vec_shift);
   uint4 v[4];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(512) cache_store_kernel(const RowArgs a) {
     const int c = t + i * gt;
     v[i] = c < n ? __ldcs(src + c) : make_uint4(0u, 0u, 0u, 0u);
   }
-  const int page = rows > 0 ? checked_page(a.table, a.table_cols, b, j, a.n_pages, a.dev_err) : -1;
+  const int page = n > 0 ? checked_page(a.table, a.table_cols, b, j, a.n_pages, a.dev_err) : -1;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) m = absmax_bits(v[i], m);
@@ -515,7 +515,7 @@ extern "C" int focus_cache_store(const focus_bf16* K, const focus_bf16* V, int B
   a.X[0] = reinterpret_cast<const uint4*>(K);
   a.X[1] = reinterpret_cast<const uint4*>(V);
   a.L = L;
-  a.cols = (L + a.page - 1) / a.page;
+  a.cols = (L - 1) / a.page + 1;
   const int gt = a.page * a.d / 32, threads = std::max(256, gt), per = threads / gt;
   auto kern = cache->format == FOCUS_CACHE_E4M3 ? cache_store_kernel<FOCUS_CACHE_E4M3> : cache_store_kernel<FOCUS_CACHE_INT8>;
   return launched(launch_k(kern, dim3((a.cols + per - 1) / per, 2 * a.H, static_cast<unsigned>(units)), dim3(threads), 0,

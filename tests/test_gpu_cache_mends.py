@@ -71,6 +71,21 @@ def test_a_call_on_a_given_stream_takes_its_workspace_there(F, sparse):
     assert all(bool((t == 7).all()) for t in taken) and torch.equal(O, want)
 
 
+# ------------------------------------------------------------------ rows
+def test_store_of_a_short_sequence_in_a_very_long_input(F):
+    """Pages that start 2^27 positions and more behind the sequence: none of their rows is read or
+    written (rows of 34 GB of memory that nothing has touched)."""
+    page, d, L = 64, 128, 2 ** 27 + 69
+    w = World(F, orc.INT8, 1, 1, 1, page, d, 2, seed=9)
+    X = torch.empty((1, 1, 1, L, d), dtype=torch.bfloat16, device=DEV)
+    X[..., :100, :] = rand_bf16((100, d), 3)
+    for n in (0, 5, 70):
+        F.focus_cache_store(X, X, w.cache, w.t_table, i32([n]))
+        for kv in range(2):
+            orc.store(X[..., :100, :].float().cpu().numpy(), w.codes[kv], w.scales[kv], w.table, [n], w.fmt)
+        w.assert_same()
+
+
 # ------------------------------------------------------------------ pages
 @pytest.mark.parametrize("cap", [0, 1, 100, 1500, 2500, 2799, 2800])
 @pytest.mark.parametrize("keeps", [[400] * 7, [400, 399, 7, 1, 0, 400, 350]])
