@@ -1612,7 +1612,9 @@ int check_attention(const focus_bf16* Q, const focus_cache* cache, const int32_t
   FOCUS_CHECK_ARG(Hq % cache->Hkv == 0, "Hq %d is not a multiple of Hkv %d", Hq, cache->Hkv);
   FOCUS_CHECK_ARG(static_cast<long long>(Hq) * qcap < (1LL << 30), "Hq * qcap must be below 2^30");
   FOCUS_CHECK_ARG(aligned16(Q) && aligned16(O), "tensors must be 16-byte aligned");
-  FOCUS_CHECK_ARG(static_cast<long long>(table_cols) * cache->page < (1LL << 31), "table of 2^31 positions or more");
+  // (room for the current block's edge, the kept blocks' slots, the sinks and the last tile behind them)
+  FOCUS_CHECK_ARG(static_cast<long long>(table_cols) * cache->page <= (1LL << 31) - (1LL << 18),
+                  "table of more than 2^31 - 2^18 positions");
   FOCUS_CHECK_ARG(scale - scale == 0.f, "scale must be finite");
   const size_t need = focus_cache_workspace_bytes(B, Hq, cache->Hkv, cache->d, qcap);
   FOCUS_CHECK_ARG(ws, "null workspace (%zu bytes needed)", need);

@@ -346,7 +346,8 @@ FOCUS_API int focus_cache_load(const focus_cache* cache, const int32_t* table, i
  * i >= n_q[b], and every row of a sequence with lens[b] <= 0, are written as zero. Q, O
  * [B, Hq, qcap, d] bf16; cache of one layer (n_mat = 1); lens [B] int32 (device).
  * ws/ws_bytes: at least focus_cache_workspace_bytes(...) bytes, 256-byte aligned; two calls
- * that may overlap on the GPU need a workspace each. Requires Hq % Hkv == 0, qcap >= 1.
+ * that may overlap on the GPU need a workspace each. Requires Hq % Hkv == 0, qcap >= 1,
+ * table_cols * page <= 2^31 - 2^18.
  */
 FOCUS_API int focus_cache_attention(const focus_bf16* Q, const int32_t* n_q, const focus_cache* cache,
                                     const int32_t* table, int table_cols, const int32_t* lens, int B, int Hq,

@@ -1,0 +1,36 @@
+"""Sizes at the ends of the cache calls' ranges are refused before any launch (CPU, pointers that
+nothing follows)."""
+import ctypes
+
+import pytest
+
+from diffusion_long_context_b200 import build as focus_build
+
+UNSUPPORTED, INVALID = -2, -1
+
+
+@pytest.fixture(scope="module")
+def F():
+    focus_build.build()
+    from diffusion_long_context_b200 import focus
+    return focus
+
+
+P = ctypes.c_void_p(4096)
+
+
+def cache_of(F, n_mat=1, n_pages=4, Hkv=1, page=16, d=64, fmt=0):
+    return ctypes.byref(F._CacheStruct(4096, 4096, 4096, 4096, n_mat, n_pages, Hkv, page, d, fmt))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_attention_over_tables_of_about_2_31_positions(F, page):
+    """Positions, page slots and sinks are counted in 32 bits, tiles of 128 at a time."""
+    before = F.launch_count()
+    for cols in (2 ** 31 // page - 1, (2 ** 31 - 2 ** 18) // page + 1):
+        st = F.lib.focus_cache_attention(P, None, cache_of(F, page=page), P, cols, P, 1, 1, 1, 0.1, P, P, 1 << 30, None)
+        assert st == INVALID and "positions" in F.last_error()
+        st = F.lib.focus_cache_sparse_attention(P, None, cache_of(F, page=page), P, cols, P, P, 16, None, 0, P, 1, 1, 1, 1, 0.1,
+                                                P, P, 1 << 30, None)
+        assert st == INVALID and "positions" in F.last_error()
+    assert F.launch_count() == before
