@@ -1583,8 +1583,9 @@ int run_cache_attention(CacheAttnArgs a, const focus_cache* c, void* ws, cudaStr
   a.n_slices = (rows + nq - 1) / nq;
   a.slice_rows = (rows + a.n_slices - 1) / a.n_slices;
   // tiles at most, for the grid and for the 32-bit tile numbers
-  const long long per_unit = SPARSE ? (static_cast<long long>((a.G + a.page - 2) / a.page + 1 + a.C) * a.page + a.S + 127) / 128
-                                    : (static_cast<long long>(a.table_cols) * a.page + 127) / 128;
+  const long long top = static_cast<long long>(a.table_cols) * a.page;      // (of G, what the table can hold)
+  const long long gen = (std::min<long long>(a.G, top) + a.page - 2) / a.page + 1;
+  const long long per_unit = SPARSE ? ((gen + a.C) * a.page + a.S + 127) / 128 : (top + 127) / 128;
   const long long most = static_cast<long long>(a.B) * a.Hkv * a.n_slices * (per_unit + kLead);
   if (most >= (1LL << 31) || static_cast<long long>(a.B) * a.Hkv * rows >= (1LL << 31)) {
     set_error("cache attention: %lld tiles of 128 keys in one call", most);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import cache_oracle as orc
-from test_gpu_cache import DEV, DTYPE, F, FMTS, PageWorld, World, i32, no_device_error, rand_bf16  # noqa: F401
+from test_gpu_cache import DEV, F, FMTS, PageWorld, World, check_attention, i32, no_device_error, rand_bf16  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,6 +41,18 @@ def test_keys_that_take_all_the_weight(F, fmt, score):
         err = np.abs(O[0, 2 * h:2 * h + 2].double().cpu().numpy() - V.mean(axis=0))
         lim = 2.0 ** -8 * (np.abs(V.mean(axis=0)) + np.abs(V).mean(axis=0))
         assert np.all(err <= lim), (h, float((err / lim).max()))
+
+
+@pytest.mark.parametrize("G", [2 ** 31 - 1, 2 ** 31 - 100, 10 ** 6])
+def test_a_current_block_far_behind_the_table_is_flagged(F, G):
+    """What lies in the table is attended, however many positions behind it the block names."""
+    w = World(F, orc.E4M3, 1, 2, 2, 16, 64, 20, seed=6)
+    Q = rand_bf16((2, 4, 3, 64), 6)
+    O = torch.zeros_like(Q)
+    P, g0 = [100, 0], [130, 0]
+    F.focus_cache_sparse_attention(Q, None, w.cache, w.t_table, i32(P), i32(g0), G, None, i32([[[1], [2]]] * 2), O)
+    check_attention(w, Q, O, None, lambda b, h: sorted({*(range(16 * (h + 1), 16 * (h + 2)) if P[b] else ()), *range(g0[b], 320)}),
+                    1 / np.sqrt(64))
 
 
 # ------------------------------------------------------------------ streams
