@@ -589,11 +589,11 @@ extern "C" int focus_pages_copy(const focus_cache* cache, const int32_t* pairs, 
   if (cache->n_mat == 0 || pair_cap == 0) return FOCUS_OK;
   const long long page_vecs = static_cast<long long>(cache->Hkv) * cache->page * cache->d / 16;
   const long long most = static_cast<long long>(pair_cap) * cache->n_mat * (2 * ((page_vecs + 1023) / 1024) + 1);
-  if (most >= (1LL << 31)) {
+  const long long grid = std::min<long long>(most, static_cast<long long>(device_sm_count()) * 8);
+  if (most + grid >= (1LL << 31)) {              // (a CTA's next piece, too, is counted in 32 bits)
     set_error("pages_copy: %d pairs of %d layers are too many for one call", pair_cap, cache->n_mat);
     return FOCUS_ERR_UNSUPPORTED;
   }
-  const long long grid = std::min<long long>(most, static_cast<long long>(device_sm_count()) * 8);
   return launched(launch_k(pages_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kCopyThreads), 0,
                            static_cast<cudaStream_t>(stream), static_cast<uint4*>(cache->k),
                            static_cast<uint4*>(cache->v), cache->k_scale, cache->v_scale, cache->n_mat, cache->n_pages,

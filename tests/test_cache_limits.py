@@ -34,3 +34,11 @@ def test_attention_over_tables_of_about_2_31_positions(F, page):
                                                 P, P, 1 << 30, None)
         assert st == INVALID and "positions" in F.last_error()
     assert F.launch_count() == before
+
+
+@pytest.mark.parametrize("n_mat,cap", [(1, (2 ** 31 - 1) // 3), (3, (2 ** 31 - 1) // 9), (1, (2 ** 31 - 1) // 3 - 300)])
+def test_copies_of_nearly_2_31_pieces(F, n_mat, cap):
+    """The pieces are walked in steps of the grid in 32 bits: the last step must not pass 2^31."""
+    before = F.launch_count()
+    assert F.lib.focus_pages_copy(cache_of(F, n_mat=n_mat), P, P, cap, None) == UNSUPPORTED
+    assert "too many" in F.last_error() and F.launch_count() == before
