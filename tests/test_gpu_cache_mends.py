@@ -43,6 +43,22 @@ def test_keys_that_take_all_the_weight(F, fmt, score):
         assert np.all(err <= lim), (h, float((err / lim).max()))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("k,q,v", [(101, -98, 58), (101, -97, -60), (-100, 98, 0), (0, 0, -80)])
+def test_keys_queries_and_values_of_extreme_size(F, fmt, k, q, v):
+    """Keys about 2^k, queries about 2^q, values about 2^v, of either format, within the header's ranges:
+    scores of a few units all the same."""
+    w = World(F, fmt, 1, 1, 2, 32, 64, 20, seed=k + 200)
+    w.scales[0] = w.scales[0] * np.float32(2.0 ** k)
+    w.scales[1] = w.scales[1] * np.float32(2.0 ** v)
+    w.upload(F)
+    Q = (rand_bf16((1, 4, 5, 64), 3).float() * 2.0 ** q).to(torch.bfloat16)
+    O = torch.zeros_like(Q)
+    F.focus_cache_attention(Q, None, w.cache, w.t_table, i32([600]), O)
+    assert bool(O.any())
+    check_attention(w, Q, O, None, lambda b, h: np.arange(600), 1 / 8)
+
+
 @pytest.mark.parametrize("G", [2 ** 31 - 1, 2 ** 31 - 100, 10 ** 6])
 def test_a_current_block_far_behind_the_table_is_flagged(F, G):
     """What lies in the table is attended, however many positions behind it the block names."""
