@@ -28,12 +28,13 @@
 // writes zeros for the units without keys. So one long sequence among short ones still fills
 // the GPU, and a sequence's length is only read on the device.
 //
-// Measured (graph replay): 32 heads of 32 rows over 32K keys 64 us, 4.2 TB/s of codes, and per
+// Measured (graph replay): 32 heads of 32 rows over 32K keys 63 us, 4.3 TB/s of codes, and per
 // doubling of the keys 5.4 TB/s (of 6.5 that a copy reaches); 9.6 us of it are there with a
 // single tile: launch, page lookup, first bytes, the chain below, output, join. What bounds a
-// long sequence is how many tiles are under way: a tile takes 4 to 5 us through memory and the
-// chain, a CTA holds four of keys and six of values in 160 KB (a ring of seven, or five of keys,
-// gained nothing more), and every stage idles for a third of the time.
+// long sequence is not one pipe or stage: a tile takes 4 to 5 us through memory and the chain,
+// every stage idles for a third of the time, half of the issue slots are used, and more tiles under
+// way than the four of keys and six of values in 160 KB (a ring of seven, or five of keys) gained
+// nothing. Which hand-over sets the 1700 cycles a tile is not known.
 //
 // A tile goes through a chain of warps, each of which works on a tile of its own, so that the
 // latencies of the hand-overs (mbarriers, tensor memory, shuffles: half of a tile's way) are
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();
-  griddep_launch_dependents();                   // (after the wait, so that what follows may read the inputs at once)
+  griddep_launch_dependents();                   // (behind the wait: the join reads lengths in front of its own)
   const uint32_t tmem = bk->tmem_base;
   const uint32_t tS = tmem, tO = tS + kS * SM::kAcc, tAcc = tO + kO * SM::kAcc, tSum = tAcc + NQ;
 
@@ -1426,8 +1427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // D / 32 dims): weights 2^(m - M) over the parts' (m, l), eight parts at a time. Units without
 // keys get zeros; units of one CTA are done already. Which parts there are follows from the
 // inputs alone, so it is worked out before the attention is done: two warps of 64 registers find
-// room beside an attention CTA. (All wait for it, those without work too: what follows in the
-// stream waits for this kernel only.)
+// room beside an attention CTA. (These inputs are read in front of the wait, which is right only
+// because the attention kernel signals behind its own wait, when all before it has been written. All
+// wait for the attention, those without work too: what follows in the stream waits for this kernel
+// only.)
 constexpr int kJoinWarps = 2;
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kJoinWarps * 32, 16) cache_combine_kernel(const CacheAttnArgs a, int NQ) {

@@ -58,7 +58,10 @@ bool pdl_enabled();
 // Launches `kernel` with programmatic stream serialization: the launch may overlap the
 // tail of the previous kernel on the stream. Every kernel of this library executes
 // griddep_wait() before it reads global memory, so results are ordered as with a plain
-// launch (and transitively so, because each kernel waits for its predecessor).
+// launch (and transitively so, because each kernel waits for its predecessor). One exception:
+// a second kernel of a call may read the call's inputs in front of its wait if the first
+// signals (griddep_launch_dependents) only behind its own wait, since all that ran before the
+// first is complete by then. cache_combine_kernel does so behind cache_attn_kernel.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                      Args&&... args) {

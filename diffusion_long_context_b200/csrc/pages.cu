@@ -3,7 +3,8 @@
 // Reference counts, tables and lists are a few thousand integers that sit in L2, and every
 // decision depends on the ones before it, so one CTA of 1024 threads plans a whole call: the
 // time is that of a few dependent memory round trips and barriers, not of bytes: 2.0 us a
-// release, 2.6 a fork (of 8 branches of 64 pages), 4.5 an own, and compacting 512 pages. Nothing
+// release, 2.6 a fork (of 8 branches of 64 pages), 4.5 an own, and compacting 512 pages; 6.9 us a
+// reserve of 8 times 64 pages and their release. Nothing
 // returns to the host; counts and the pairs that focus_pages_copy has to copy stay on the
 // device. Free pages are ranked by block-wide scans in ascending order, so that the result
 // never depends on which thread came first.

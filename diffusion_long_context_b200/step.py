@@ -39,7 +39,9 @@ class SparseStep:
 
         cache: torch.float8_e4m3fn or torch.int8, hold keys and values in the 8-bit paged cache.
         K and V are then what block_entry() stores; the steps read the cache alone (the layer
-        that finds the sinks through one bf16 copy of its rows), each sparse layer by two calls."""
+        that finds the sinks through one bf16 copy of its rows, made in every step), each sparse
+        layer by two calls. K and V stay with the caller, and the cache comes on top of them; a
+        32K step takes 1.54 ms this way, 1.03 ms without."""
         c = cfg
         self.cfg = c
         self.fused = fused

@@ -271,7 +271,7 @@ FOCUS_API int focus_sparse_attention_noalloc(const focus_bf16* Q_active, const i
  * ---------------------------------------------------------------- 8-bit paged cache
  * The approximate KV cache (Focus-dLLM summary page, "近似KV缓存") held in 8 bits, in pages of
  * `page` positions that sequences can share. The pages describe a cache of the model's own
- * type only; this form halves the bytes that every attention of a step reads.
+ * type only; this form halves the bytes that an attention over it reads.
  *
  * Codes k, v [n_mat, n_pages, Hkv, page, d] (n_mat layers) with one fp32 scale for each
  * layer, page and head, k_scale, v_scale [n_mat, n_pages, Hkv]: an element stands for
@@ -280,6 +280,9 @@ FOCUS_API int focus_sparse_attention_noalloc(const focus_bf16* Q_active, const i
  * it, a code the nearest (ties to even) to x / s, both divisions rounded in fp32; s = 0 (a
  * page of zeros) gives codes 0. Values must be finite: a NaN or an infinity makes the scale
  * of its page and head NaN or infinite, and what reads that page NaN.
+ * The attention's products of codes are scaled in fp32: keys below 2^106 and values below 2^64 in
+ * magnitude stay finite on the way, and scores may be of any finite size. Of int8, a row of
+ * queries whose largest is below 1e-30 counts as a row of zeros.
  *
  * table [B, table_cols] int32 (device): page table[b, j] holds the positions
  * [j * page, (j + 1) * page) of sequence b. Entries that a call needs must lie in
@@ -419,7 +422,8 @@ FOCUS_API int focus_pages_compact(const focus_pages* pages, int32_t* pairs, int 
 
 /* Codes and scales of page pairs[r, 0] to page pairs[r, 1], r < min(n_pairs[0], pair_cap), in
  * all n_mat layers. No page may be both source and target, or target twice. Pairs outside
- * [0, n_pages) are skipped and flagged. */
+ * [0, n_pages) are skipped and flagged. A call of 2^31 pieces of 16 KB, or nearly as many, is
+ * refused (FOCUS_ERR_UNSUPPORTED). */
 FOCUS_API int focus_pages_copy(const focus_cache* cache, const int32_t* pairs, const int32_t* n_pairs, int pair_cap,
                                void* stream);
 
