@@ -42,3 +42,13 @@ def test_copies_of_nearly_2_31_pieces(F, n_mat, cap):
     before = F.launch_count()
     assert F.lib.focus_pages_copy(cache_of(F, n_mat=n_mat), P, P, cap, None) == UNSUPPORTED
     assert "too many" in F.last_error() and F.launch_count() == before
+
+
+def test_owning_lists_that_name_2_31_table_entries(F):
+    """The entries of all listed ranges are counted in 32 bits, a sequence that is listed again anew."""
+    pages = ctypes.byref(F._PagesStruct(4096, 4096, 4096, 1 << 20, 2, 1 << 22))
+    before = F.launch_count()
+    assert F.lib.focus_pages_own(pages, P, P, P, 1024, P, 16, P, P, None) == UNSUPPORTED
+    assert "entries" in F.last_error()
+    assert F.lib.focus_pages_own(pages, P, P, P, 512, P, 16, P, P, None) == UNSUPPORTED
+    assert F.launch_count() == before
