@@ -463,8 +463,8 @@ extern "C" int focus_pages_own(const focus_pages* pages, const int32_t* seqs, co
   if (const int st = check_pages(pages, n)) return st;
   FOCUS_CHECK_ARG(n_pairs && status && (n == 0 || (seqs && first && last)), "null pointer argument");
   FOCUS_CHECK_ARG(pair_cap >= 0 && (pair_cap == 0 || pairs), "bad pairs");
-  if (static_cast<long long>(n) * pages->table_cols >= (1LL << 31)) {      // (entries are counted in 32 bits)
-    set_error("pages_own: %d ranges of up to %d entries, 2^31 or more in all", n, pages->table_cols);
+  if (static_cast<long long>(n) * pages->table_cols >= (1LL << 31) - kPageThreads) {   // (counted in 32 bits, a pass beyond the last)
+    set_error("pages_own: %d ranges of up to %d entries, nearly 2^31 or more in all", n, pages->table_cols);
     return FOCUS_ERR_UNSUPPORTED;
   }
   PageArgs a = page_args(pages, seqs, first, last, n);

@@ -404,7 +404,7 @@ FOCUS_API int focus_pages_fork(const focus_pages* pages, const int32_t* src, con
  * replaced by free pages; pairs[r] = (shared page, own page), r < n_pairs[0], is what
  * focus_pages_copy has to copy. Of a page that every one of its sequences is listed with,
  * the last in the list keeps it. pairs [pair_cap, 2], n_pairs [1]. A call that is short sets
- * n_pairs to 0 and leaves what it has tried in pairs. Requires n * table_cols < 2^31. */
+ * n_pairs to 0 and leaves what it has tried in pairs. Requires n * table_cols < 2^31 - 1024. */
 FOCUS_API int focus_pages_own(const focus_pages* pages, const int32_t* seqs, const int32_t* first,
                               const int32_t* last, int n, int32_t* pairs, int pair_cap, int32_t* n_pairs,
                               int32_t* status, void* stream);

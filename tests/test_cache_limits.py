@@ -51,4 +51,6 @@ def test_owning_lists_that_name_2_31_table_entries(F):
     assert F.lib.focus_pages_own(pages, P, P, P, 1024, P, 16, P, P, None) == UNSUPPORTED
     assert "entries" in F.last_error()
     assert F.lib.focus_pages_own(pages, P, P, P, 512, P, 16, P, P, None) == UNSUPPORTED
+    pages = ctypes.byref(F._PagesStruct(4096, 4096, 4096, 1 << 20, 1, 2 ** 31 - 1000))      # (the step behind the last entry)
+    assert F.lib.focus_pages_own(pages, P, P, P, 1, P, 16, P, P, None) == UNSUPPORTED
     assert F.launch_count() == before
