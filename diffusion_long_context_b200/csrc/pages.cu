@@ -253,8 +253,45 @@ __global__ void __launch_bounds__(kPageThreads) pages_release_kernel(const PageA
 // needs a copy when enough others keep x: its rank among this chunk's entries of x is below
 // refs[x] - 1, refs[x] already reduced by the chunks before. Until enough free pages are known
 // to exist, pairs[r] holds (x, table slot) and can be undone.
+struct OwnLists {
+  int seq[kMaxList], first[kMaxList], last[kMaxList], pre[kMaxList + 1];   // pre: entries of the ranges before
+};
+
+// Place in the table of entry e of the listed ranges, -1 if an earlier range holds it too.
+__device__ __forceinline__ int listed_entry(const PageArgs& a, const OwnLists& l, int e) {
+  int lo = 0, hi = a.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.pre[mid] <= e) lo = mid;
+    else hi = mid - 1;
+  }
+  const int j = l.first[lo] + (e - l.pre[lo]);
+  bool again = false;
+  for (int o = 0; o < lo; ++o) again |= l.seq[o] == l.seq[lo] && j >= l.first[o] && j < l.last[o];
+  return again ? -1 : l.seq[lo] * a.cols + j;
+}
+
+// The copies that a call without room for all its pairs needs (this thread's part of their number).
+// Copies without a pair have not lowered their page's count, so what the walk found behind them is
+// too high. All m entries of a page are taken off its count R and put back one by one; min(m, R - 1)
+// of them, the copies, find another one there. (Not inlined: in the kernel's path it cost 2 us.)
+__device__ __noinline__ int count_copies(const PageArgs& a, const OwnLists& l, int entries) {
+  int copies = 0;
+  for (int back = 0; back < 2; ++back) {
+    for (int e = threadIdx.x; e < entries; e += kPageThreads) {
+      const int slot = listed_entry(a, l, e);
+      const int x = slot >= 0 ? a.table[slot] : -1;
+      if (x < 0 || x >= a.n_pages) continue;
+      const int was = atomicAdd(&a.refs[x], back ? 1 : -1);
+      if (back && was >= 1) ++copies;
+    }
+    __syncthreads();
+  }
+  return copies;
+}
+
 __global__ void __launch_bounds__(kPageThreads) pages_own_kernel(const PageArgs a) {
-  __shared__ int s_seq[kMaxList], s_first[kMaxList], s_last[kMaxList], s_pre[kMaxList + 1];
+  __shared__ OwnLists l;
   __shared__ int s_x[kPageThreads], s_warp[32];
   griddep_wait();
   griddep_launch_dependents();
@@ -266,38 +303,30 @@ __global__ void __launch_bounds__(kPageThreads) pages_own_kernel(const PageArgs 
     if (!ok) flag(a);
     const int first = max(0, a.list[1][i]);
     const int last = ok ? min(a.list[2][i], min(a.held[seq], a.cols)) : 0;
-    s_seq[i] = ok ? seq : -1;
-    s_first[i] = first;
-    s_last[i] = last;
+    l.seq[i] = ok ? seq : -1;
+    l.first[i] = first;
+    l.last[i] = last;
     cnt = max(0, last - first);
   }
   int entries = 0;
   const int pre = block_scan(cnt, s_warp, &entries);
-  if (i < a.n) s_pre[i] = pre;
-  if (i == 0) s_pre[a.n] = entries;
+  if (i < a.n) l.pre[i] = pre;
+  if (i == 0) l.pre[a.n] = entries;
   __syncthreads();
-  // Entry e of the listed ranges: its page (-1: none, or listed before) and its place in the table.
-  auto entry = [&](int e, int& slot, bool report) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_pre[mid] <= e) lo = mid;
-      else hi = mid - 1;
-    }
-    const int j = s_first[lo] + (e - s_pre[lo]);
-    for (int o = 0; o < lo; ++o)
-      if (s_seq[o] == s_seq[lo] && j >= s_first[o] && j < s_last[o]) return -1;
-    slot = s_seq[lo] * a.cols + j;
-    const int x = a.table[slot];
-    if (x >= 0 && x < a.n_pages) return x;
-    if (report) flag(a);
-    return -1;
-  };
   int found = 0;                         // copies needed so far (the same in every thread)
   for (int e0 = 0; e0 < entries; e0 += kPageThreads) {
     const int e = e0 + i;
-    int slot = -1;
-    const int x = e < entries ? entry(e, slot, true) : -1;
+    int x = -1, slot = -1;
+    if (e < entries) {
+      slot = listed_entry(a, l, e);
+      if (slot >= 0) {
+        x = a.table[slot];
+        if (x < 0 || x >= a.n_pages) {
+          flag(a);
+          x = -1;
+        }
+      }
+    }
     s_x[i] = x;
     __syncthreads();
     bool copies = false;
@@ -321,22 +350,9 @@ __global__ void __launch_bounds__(kPageThreads) pages_own_kernel(const PageArgs 
   __syncthreads();
   if (found > room) {
     for (int r = i; r < min(found, a.pair_cap); r += kPageThreads) atomicAdd(&a.refs[a.pairs[2 * r]], 1);
-    if (found > a.pair_cap) {
-      // Copies without a pair have not lowered their page's count, so what came after them was
-      // counted too high. Counted anew: all m entries of a page are taken off its count R and put
-      // back one by one; min(m, R - 1) of them, the copies, find another one there.
+    if (found > a.pair_cap) {            // (counted too high, see count_copies)
       __syncthreads();
-      int slot = -1, copies = 0;
-      for (int e = i; e < entries; e += kPageThreads) {
-        const int x = entry(e, slot, false);
-        if (x >= 0) atomicSub(&a.refs[x], 1);
-      }
-      __syncthreads();
-      for (int e = i; e < entries; e += kPageThreads) {
-        const int x = entry(e, slot, false);
-        if (x >= 0 && atomicAdd(&a.refs[x], 1) >= 1) ++copies;
-      }
-      block_scan(copies, s_warp, &found);
+      block_scan(count_copies(a, l, entries), s_warp, &found);
     }
     if (i == 0) {
       *a.status = found - room;
@@ -463,7 +479,8 @@ extern "C" int focus_pages_own(const focus_pages* pages, const int32_t* seqs, co
   if (const int st = check_pages(pages, n)) return st;
   FOCUS_CHECK_ARG(n_pairs && status && (n == 0 || (seqs && first && last)), "null pointer argument");
   FOCUS_CHECK_ARG(pair_cap >= 0 && (pair_cap == 0 || pairs), "bad pairs");
-  if (static_cast<long long>(n) * pages->table_cols >= (1LL << 31) - kPageThreads) {   // (counted in 32 bits, a pass beyond the last)
+  if (static_cast<long long>(n) * pages->table_cols >= (1LL << 31) - kPageThreads) {
+    // (entries are counted in 32 bits, and a pass behind the last)
     set_error("pages_own: %d ranges of up to %d entries, nearly 2^31 or more in all", n, pages->table_cols);
     return FOCUS_ERR_UNSUPPORTED;
   }
